@@ -11,7 +11,10 @@ Names follow the C ABI: ``ultraep_create``, ``ultraep_balance``,
 ``ultraep_balance_static``,
 ``ultraep_dispatch_layout``, ``ultraep_permute``, ``ultraep_combine``,
 ``ultraep_combine_backward``, ``ultraep_weight_sync_plan``,
-``ultraep_weight_sync``, ``ultraep_fold_grads``.
+``ultraep_weight_sync``, ``ultraep_fold_grads``; and of the experts' own steps
+(``include/ultraep_experts.h``) ``ultraep_permute_quant``,
+``ultraep_weight_quant``, ``ultraep_expert_gemm``, ``ultraep_expert_wgrad``,
+``ultraep_grad_sumsq``, ``ultraep_grad_clip``.
 """
 from __future__ import annotations
 
@@ -82,6 +85,19 @@ _SIGNATURES = {
     "ultraep_status_string": (ctypes.c_char_p, [ctypes.c_int]),
 }
 
+# include/ultraep_experts.h
+_EXPERT_SIGNATURES = {
+    "ultraep_permute_quant": (_I32, [_P, _P, _P, _I32, _P, _I64, _I32, _I32, _I32, _P, _P, _P, _P, _I64, _I64, _P]),
+    "ultraep_weight_quant": (_I32, [_P, _P, _I32, _I32, _I32, _P, _P, _P, _P, _P]),
+    "ultraep_expert_gemm": (_I32, [_P, _P, _P, _P, _I32, _P, _P, _I32, _I32, _I32, _P, _I64, _P]),
+    "ultraep_expert_wgrad": (_I32, [_P, _P, _P, _P, _I32, _P, _P, _I32, _I32, _I32, _I64, _P, _I32, _P]),
+    "ultraep_grad_sumsq": (_I32, [_P, _P, _P, _I32, _I32, _P, _I32, _P, _SZ, _P]),
+    "ultraep_grad_clip": (_I32, [_P, _P, _P, _I32, _I32, _P, ctypes.c_double, _P, _P, _P]),
+}
+QUANT_BLOCK = 128
+MAX_GRAD_TENSORS = 4096
+GRAD_WORKSPACE_BYTES = 16384
+
 
 def lib() -> ctypes.CDLL:
     """Load libultraep.so (built in place by ``__graft_entry__.build()``)."""
@@ -91,7 +107,7 @@ def lib() -> ctypes.CDLL:
             raise RuntimeError(f"{LIB_PATH} is missing: build it with `python -c 'import "
                                "__graft_entry__ as g; g.build()'` (needs hipcc for gfx950)")
         handle = ctypes.CDLL(LIB_PATH)
-        for name, (res, args) in _SIGNATURES.items():
+        for name, (res, args) in {**_SIGNATURES, **_EXPERT_SIGNATURES}.items():
             fn = getattr(handle, name)
             fn.restype = res
             fn.argtypes = args
@@ -257,6 +273,158 @@ def ultraep_weight_sync(ctx: Context, plan, master_ptrs, replica_weights, numel:
     st = lib().ultraep_weight_sync(ctx.handle, _ptr(plan), _ptr(master_ptrs), _ptr(replica_weights), numel,
                                    slot_begin, slot_end, _ptr(relay), _stream(stream))
     _check("ultraep_weight_sync", st)
+
+
+# The experts' steps.  Unlike the calls above, whose buffers are plain arrays,
+# these take buffers whose padded shapes are part of the format, so the binding
+# checks shapes, types and the device before it hands out their addresses.
+def quant_pitch(H: int) -> int:
+    """Bytes of a quantised row of H columns (H rounded up to 128)."""
+    return -(-H // QUANT_BLOCK) * QUANT_BLOCK
+
+
+def quant_scale_pitch(H: int) -> int:
+    """Scale bytes of a quantised row of H columns (its blocks, rounded up to 4)."""
+    return -(-(-(-H // QUANT_BLOCK)) // 4) * 4
+
+
+def quant_blocks(rows: int, experts: int) -> int:
+    """Blocks the columns form of `rows` rows of `experts` experts needs."""
+    return rows // QUANT_BLOCK + experts
+
+
+def pointer_table(tensors, device="cuda"):
+    """int64 device tensor of the tensors' addresses (None: a NULL entry)."""
+    import torch
+    return torch.tensor([0 if t is None else t.data_ptr() for t in tensors], dtype=torch.int64).to(device)
+
+
+def _is(t, dtypes, shape) -> bool:
+    """A contiguous tensor of the current device with one of the types and this shape (None: any extent)."""
+    import torch
+    return (t.is_cuda and t.device.index == torch.cuda.current_device() and t.dtype in dtypes and t.is_contiguous()
+            and len(t.shape) == len(shape) and all(w is None or n == w for n, w in zip(t.shape, shape)))
+
+
+def _need(fn: str, *ok) -> None:
+    if not all(ok):
+        raise UltraEPError(fn, -1)
+
+
+def _types():
+    import torch
+    return ({torch.uint8, torch.float8_e4m3fn}, {torch.bfloat16, torch.int16, torch.uint16}, {torch.int64}, {torch.int32})
+
+
+def ultraep_permute_quant(ctx: Context, plan, inv, k: int, hidden, p_begin: int, p_end: int, q=None, q_scale=None,
+                          qt=None, qt_scale=None, rows: Optional[int] = None, stream=None) -> None:
+    """Rows gathered into the layout (inv None: taken in order) and quantised.
+
+    hidden bf16 [., H]; q [rows, quant_pitch(H)] with q_scale [rows, quant_scale_pitch(H)] the rows form,
+    qt [blocks, H, 128] with qt_scale [blocks, H] the columns form.  `rows` is the segment's capacity,
+    by default q's rows (with qt alone it has to be given)."""
+    fn = "ultraep_permute_quant"
+    f8, f16, _, i32 = _types()
+    _need(fn, (q is None) == (q_scale is None), (qt is None) == (qt_scale is None), q is not None or qt is not None,
+          _is(hidden, f16, (None, None)), inv is None or (inv.is_cuda and inv.dtype in i32 and inv.is_contiguous()))
+    H = hidden.shape[1]
+    if rows is None:
+        _need(fn, q is not None)
+        rows = q.shape[0]
+    if q is not None:
+        _need(fn, _is(q, f8, (None, quant_pitch(H))), _is(q_scale, f8, (q.shape[0], quant_scale_pitch(H))),
+              rows <= q.shape[0])
+    blocks = 0
+    if qt is not None:
+        blocks = qt.shape[0]
+        _need(fn, _is(qt, f8, (None, H, QUANT_BLOCK)), _is(qt_scale, f8, (blocks, H)))
+    st = lib().ultraep_permute_quant(ctx.handle, _ptr(plan), _ptr(inv), k, _ptr(hidden), hidden.shape[0], H, p_begin,
+                                     p_end, _ptr(q), _ptr(q_scale), _ptr(qt), _ptr(qt_scale), rows, blocks,
+                                     _stream(stream))
+    _check(fn, st)
+
+
+def ultraep_weight_quant(ctx: Context, weights, n: int, N: int, K: int, q=None, q_scale=None, qt=None, qt_scale=None,
+                         stream=None) -> None:
+    """weights: int64 device tensor [n] of pointers to bf16 [N, K]; q [n, N, quant_pitch(K)] with q_scale
+    [n, ceil(N/128), quant_scale_pitch(K)], and the transposes' qt [n, K, quant_pitch(N)] with qt_scale."""
+    fn = "ultraep_weight_quant"
+    f8, _, i64, _ = _types()
+    _need(fn, (q is None) == (q_scale is None), (qt is None) == (qt_scale is None), _is(weights, i64, (None,)),
+          weights.shape[0] >= n)
+    for a, b, x, xs in ((N, K, q, q_scale), (K, N, qt, qt_scale)):
+        if x is not None:
+            _need(fn, _is(x, f8, (None, a, quant_pitch(b))),
+                  _is(xs, f8, (None, quant_pitch(a) // QUANT_BLOCK, quant_scale_pitch(b))),
+                  x.shape[0] >= n, xs.shape[0] >= n)
+    st = lib().ultraep_weight_quant(ctx.handle, _ptr(weights), n, N, K, _ptr(q), _ptr(q_scale), _ptr(qt),
+                                    _ptr(qt_scale), _stream(stream))
+    _check(fn, st)
+
+
+def ultraep_expert_gemm(ctx: Context, plan, q, q_scale, K: int, w, w_scale, N: int, p_begin: int, p_end: int, out,
+                        stream=None) -> None:
+    """out[i] = row i times its expert's weights, bf16 [rows, N].
+
+    w, w_scale: int64 device tensors [p_end - p_begin] of pointers to the quantised weights and scales."""
+    fn = "ultraep_expert_gemm"
+    f8, f16, i64, _ = _types()
+    _need(fn, _is(q, f8, (None, quant_pitch(K))), _is(q_scale, f8, (q.shape[0], quant_scale_pitch(K))),
+          _is(w, i64, (None,)), _is(w_scale, i64, (None,)), w.shape[0] >= p_end - p_begin,
+          w_scale.shape[0] >= p_end - p_begin, _is(out, f16, (None, N)))
+    st = lib().ultraep_expert_gemm(ctx.handle, _ptr(plan), _ptr(q), _ptr(q_scale), K, _ptr(w), _ptr(w_scale), N,
+                                   p_begin, p_end, _ptr(out), min(out.shape[0], q.shape[0]), _stream(stream))
+    _check(fn, st)
+
+
+def ultraep_expert_wgrad(ctx: Context, plan, dyt, dyt_scale, N: int, xt, xt_scale, K: int, p_begin: int, p_end: int,
+                         rows: int, grads, accumulate: bool = False, stream=None) -> None:
+    """grads: int64 device tensor [p_end - p_begin] of pointers to fp32 [N, K]; rows: the segment's capacity."""
+    fn = "ultraep_expert_wgrad"
+    f8, _, i64, _ = _types()
+    _need(fn, rows >= 0, _is(dyt, f8, (None, N, QUANT_BLOCK)), _is(dyt_scale, f8, (dyt.shape[0], N)),
+          _is(xt, f8, (None, K, QUANT_BLOCK)), _is(xt_scale, f8, (xt.shape[0], K)),
+          min(dyt.shape[0], xt.shape[0]) >= quant_blocks(rows, p_end - p_begin), _is(grads, i64, (None,)),
+          grads.shape[0] >= p_end - p_begin)
+    st = lib().ultraep_expert_wgrad(ctx.handle, _ptr(plan), _ptr(dyt), _ptr(dyt_scale), N, _ptr(xt), _ptr(xt_scale), K,
+                                    p_begin, p_end, rows, _ptr(grads), int(accumulate), _stream(stream))
+    _check(fn, st)
+
+
+def _grad_dtype(fn: str, dtype) -> int:
+    import torch
+    _need(fn, dtype in (torch.float32, torch.bfloat16))
+    return int(dtype == torch.bfloat16)
+
+
+def ultraep_grad_sumsq(ctx: Context, tensors, numels, n: int, dtype, sumsq, workspace, accumulate: bool = False,
+                       stream=None) -> None:
+    """sumsq (fp64 [1]) = or += the squares of n tensors' elements (tensors, numels: int64 device tensors;
+    workspace: GRAD_WORKSPACE_BYTES)."""
+    import torch
+    fn = "ultraep_grad_sumsq"
+    i64 = _types()[2]
+    _need(fn, _is(tensors, i64, (None,)), _is(numels, i64, (None,)), min(tensors.shape[0], numels.shape[0]) >= n,
+          _is(sumsq, {torch.float64}, (1,)), workspace.is_cuda)
+    st = lib().ultraep_grad_sumsq(ctx.handle, _ptr(tensors), _ptr(numels), n, _grad_dtype(fn, dtype), _ptr(sumsq),
+                                  int(accumulate), _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                  _stream(stream))
+    _check(fn, st)
+
+
+def ultraep_grad_clip(ctx: Context, tensors, numels, n: int, dtype, sumsq, max_norm: float, norm=None, out=None,
+                      stream=None) -> None:
+    """Scale n tensors to a global norm of at most max_norm, in place or into the tensors `out` points to;
+    norm (fp32 [1], optional) receives the norm before."""
+    import torch
+    fn = "ultraep_grad_clip"
+    i64 = _types()[2]
+    _need(fn, _is(tensors, i64, (None,)), _is(numels, i64, (None,)), min(tensors.shape[0], numels.shape[0]) >= n,
+          _is(sumsq, {torch.float64}, (1,)), norm is None or _is(norm, {torch.float32}, (1,)),
+          out is None or (_is(out, i64, (None,)) and out.shape[0] >= n))
+    st = lib().ultraep_grad_clip(ctx.handle, _ptr(tensors), _ptr(numels), n, _grad_dtype(fn, dtype), _ptr(sumsq),
+                                 float(max_norm), _ptr(norm), _ptr(out), _stream(stream))
+    _check(fn, st)
 
 
 def status_string(status: int) -> str:

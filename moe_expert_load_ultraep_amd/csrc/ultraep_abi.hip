@@ -12,16 +12,12 @@
 #include "ultraep.h"
 #include "ultraep_internal.h"
 
-struct ultraep_ctx {
-  ultraep::Shape sh;
-};
-
 namespace {
 
+using ultraep::aligned;
+using ultraep::from_hip;
 using ultraep::PlanLayout;
 using ultraep::Shape;
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 void build_layout(Shape* sh) {
   PlanLayout& L = sh->lay;
@@ -59,8 +55,6 @@ int pairs_per_layer(const ultraep_ctx* ctx, int64_t T, int32_t k, int32_t* N) {
   *N = static_cast<int32_t>(n);
   return ULTRAEP_OK;
 }
-
-int from_hip(hipError_t e) { return e == hipSuccess ? ULTRAEP_OK : ULTRAEP_ELAUNCH; }
 
 // Workspace of ultraep_balance_static.  Every device the library runs on
 // holds its own copy from the time the code object is loaded there until the

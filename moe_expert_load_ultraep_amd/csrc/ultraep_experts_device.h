@@ -1,0 +1,97 @@
+// Device helpers of the experts' kernels: the segment's groups and the
+// 8-bit block format (include/ultraep_experts.h).  Internal.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "ultraep_device.h"
+
+namespace ultraep {
+namespace {
+
+constexpr int kQBlock = 128;  // values per scale
+
+__host__ __device__ inline int32_t ceil_div(int32_t a, int32_t b) { return (a + b - 1) / b; }
+// Row pitch of the rows and weights forms, and of their scales.
+__host__ __device__ inline int32_t q_pitch(int32_t H) { return ceil_div(H, kQBlock) * kQBlock; }
+__host__ __device__ inline int32_t s_pitch(int32_t H) { return ceil_div(ceil_div(H, kQBlock), 4) * 4; }
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+// First row of the range's expert p, counted from the range's first row and
+// never beyond the rows that are there.
+__device__ __forceinline__ int32_t group_row(const int32_t* off, int32_t p, int64_t cap) {
+  const int64_t o = static_cast<int64_t>(off[p]) - off[0];
+  return static_cast<int32_t>(max(min(o, cap), int64_t{0}));
+}
+
+// Tiles of `unit` rows: expert p's start at first(p) = row(p) / unit + p, so
+// first(p + 1) - first(p) >= ceil(rows of p / unit) without any prefix sum
+// (at most one tile an expert stays empty).  The expert of tile t is the last
+// p with first(p) <= t; every wave finds it by itself, 64 experts a step.
+// Every lane must be active; the result is wave-uniform.
+__device__ __forceinline__ int32_t find_group(const int32_t* off, int32_t ne, int64_t cap, int32_t unit,
+                                              int32_t t) {
+  int32_t n = 0;
+  for (int32_t p0 = 0; p0 < ne; p0 += 64) {
+    const int32_t p = p0 + lane_id();
+    const bool before = p < ne && group_row(off, min(p, ne - 1), cap) / unit + p <= t;
+    const int32_t got = static_cast<int32_t>(__builtin_popcountll(ballot(before)));
+    n += got;
+    if (got < 64) break;
+  }
+  return __builtin_amdgcn_readfirstlane(n - 1);
+}
+
+// Exponent of a block whose largest finite magnitude has these float bits:
+// the smallest e >= -126 with amax <= 448 * 2^e = 1.75 * 2^(8 + e), 0 for a
+// block without a finite value other than zero.
+__device__ __forceinline__ int32_t block_exponent(uint32_t amax) {
+  const int32_t e = static_cast<int32_t>(amax >> 23) - 135 + ((amax & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  return amax == 0 ? 0 : max(e, -126);
+}
+
+// 2^-e for e in [-126, 120].
+__device__ __forceinline__ float inverse_scale(int32_t e) {
+  return __builtin_bit_cast(float, static_cast<uint32_t>(127 - e) << 23);
+}
+
+// Magnitude bits of a bf16 pair's low or high value as a float's; 0 when it is
+// not finite.  Magnitudes order as their bits do.
+__device__ __forceinline__ uint32_t finite_bits(uint32_t v) {
+  const uint32_t m = v & 0x7FFFFFFFu;
+  return m < 0x7F800000u ? m : 0u;
+}
+
+__device__ __forceinline__ uint32_t amax_of(const u32x4& x) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = max(m, max(finite_bits(x[i] << 16), finite_bits(x[i] & 0xFFFF0000u)));
+  return m;
+}
+
+// Largest of 16 lanes (one aligned row), in every lane.
+__device__ __forceinline__ uint32_t row16_max(uint32_t x) {
+  x = max(x, dpp<0xB1>(x));
+  x = max(x, dpp<0x4E>(x));
+  x = max(x, dpp<0x141>(x));
+  return max(x, dpp<0x140>(x));
+}
+
+// Eight bf16 times a power of two, rounded to nearest even e4m3 (infinities
+// and NaN give NaN; nothing else is above 448).
+__device__ __forceinline__ u32x2 to_e4m3(const u32x4& x, float s) {
+  u32x2 y;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    int v = __builtin_amdgcn_cvt_pk_fp8_f32(bf16_lo(x[2 * i]) * s, bf16_hi(x[2 * i]) * s, 0, false);
+    v = __builtin_amdgcn_cvt_pk_fp8_f32(bf16_lo(x[2 * i + 1]) * s, bf16_hi(x[2 * i + 1]) * s, v, true);
+    y[i] = static_cast<uint32_t>(v);
+  }
+  return y;
+}
+
+}  // namespace
+}  // namespace ultraep

@@ -1,0 +1,232 @@
+// gfx950 kernels of the gradients' global norm and clipping
+// (include/ultraep_experts.h): sum of squares over many tensors, and scaling
+// them.
+//
+// Both walk the tensors' chunks of kGradBytes: a workgroup scans the tensors'
+// chunk counts into LDS once and takes one contiguous share of all chunks, so
+// tensors of any sizes spread evenly and the order of every sum depends on the
+// sizes alone.  HBM-streaming; the squares are added in fp64 (the vector units
+// do fp64 at the fp32 rate of one lane, far above what HBM feeds them), so no
+// square overflows and long sums lose nothing.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "ultraep_device.h"
+#include "ultraep_experts.h"
+#include "ultraep_internal.h"
+
+namespace ultraep {
+namespace {
+
+constexpr int kGradThreads = 256;
+constexpr int kGradVecs = 4;                                 // 16-byte vectors in flight per lane
+constexpr int kGradBytes = kGradThreads * kGradVecs * 16;    // bytes of a chunk
+constexpr int kGradBlocks = ULTRAEP_GRAD_WORKSPACE_BYTES / 8;  // partial sums
+
+// Vectors at any alignment of their elements.
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+
+struct Share {
+  int64_t begin, end;  // chunks of this workgroup
+  int32_t tensor;      // the tensor `begin` lies in
+};
+
+// first[t]: chunks of the tensors before t.  Returns the workgroup's share.
+__device__ Share grad_share(const void* const* tensors, const int64_t* numels, int32_t n, int32_t per_chunk,
+                            int64_t* first) {
+  __shared__ int64_t s_wave[kGradThreads / 64];
+  const int tid = threadIdx.x, lane = lane_id(), wv = tid >> 6;
+  const int32_t each = (n + kGradThreads - 1) / kGradThreads;
+  const int32_t t0 = min(tid * each, n), t1 = min(t0 + each, n);
+  int64_t sum = 0;
+  for (int32_t t = t0; t < t1; ++t) {
+    first[t] = sum;
+    const int64_t m = tensors[t] == nullptr ? 0 : numels[t];
+    sum += m > 0 ? (m + per_chunk - 1) / per_chunk : 0;
+  }
+  int64_t scan = sum;  // inclusive over the wave
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int64_t y = __shfl_up(scan, d);
+    if (lane >= d) scan += y;
+  }
+  if (lane == 63) s_wave[wv] = scan;
+  __syncthreads();
+  int64_t before = scan - sum, total = 0;
+#pragma unroll
+  for (int i = 0; i < kGradThreads / 64; ++i) {
+    if (i < wv) before += s_wave[i];
+    total += s_wave[i];
+  }
+  for (int32_t t = t0; t < t1; ++t) first[t] += before;
+  __syncthreads();
+  Share sh;
+  const int64_t each_wg = (total + gridDim.x - 1) / gridDim.x;
+  sh.begin = min(each_wg * blockIdx.x, total);
+  sh.end = min(sh.begin + each_wg, total);
+  int32_t lo = 0, hi = n;  // last tensor whose first chunk is at or before begin
+  while (hi - lo > 1) {
+    const int32_t mid = (lo + hi) >> 1;
+    if (first[mid] <= sh.begin) lo = mid; else hi = mid;
+  }
+  sh.tensor = lo;
+  return sh;
+}
+
+__device__ __forceinline__ float f32_of(uint32_t bits) { return __builtin_bit_cast(float, bits); }
+__device__ __forceinline__ uint32_t bits_of(float v) { return __builtin_bit_cast(uint32_t, v); }
+
+__device__ __forceinline__ float scaled(double c, float v) { return static_cast<float>(c * static_cast<double>(v)); }
+
+__device__ __forceinline__ double square(float v) { return static_cast<double>(v) * static_cast<double>(v); }
+
+// Sum of the squares of one vector's values.
+template <bool BF16>
+__device__ __forceinline__ double squares(const u32x4& v) {
+  double s = 0.0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (BF16) {
+      s += square(bf16_lo(v[i]));
+      s += square(bf16_hi(v[i]));
+    } else {
+      s += square(f32_of(v[i]));
+    }
+  }
+  return s;
+}
+
+__device__ __forceinline__ double wave_sum_f64(double x) {
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) x += __shfl_xor(x, d);
+  return x;
+}
+
+// Sum over the workgroup, in thread 0.
+__device__ double block_sum_f64(double x) {
+  __shared__ double s_sum[kGradThreads / 64];
+  x = wave_sum_f64(x);
+  if (lane_id() == 0) s_sum[threadIdx.x >> 6] = x;
+  __syncthreads();
+  return ((s_sum[0] + s_sum[1]) + s_sum[2]) + s_sum[3];
+}
+
+template <bool BF16>
+__global__ __launch_bounds__(kGradThreads) void grad_sumsq_kernel(const void* const* __restrict__ tensors,
+                                                                  const int64_t* __restrict__ numels, int32_t n,
+                                                                  double* __restrict__ partial) {
+  extern __shared__ int64_t s_first[];
+  constexpr int kVec = BF16 ? 8 : 4, kChunk = kGradBytes / (BF16 ? 2 : 4);
+  const Share sh = grad_share(tensors, numels, n, kChunk, s_first);
+  double acc = 0.0;
+  int32_t t = sh.tensor;
+  for (int64_t c = sh.begin; c < sh.end; ++c) {
+    while (t + 1 < n && s_first[t + 1] <= c) ++t;
+    const int64_t at = (c - s_first[t]) * kChunk, len = min(numels[t] - at, static_cast<int64_t>(kChunk));
+    const char* p = static_cast<const char*>(tensors[t]) + at * (BF16 ? 2 : 4);
+    u32x4 v[kGradVecs];
+#pragma unroll
+    for (int u = 0; u < kGradVecs; ++u) {
+      const int i = (u * kGradThreads + static_cast<int>(threadIdx.x)) * kVec;
+      v[u] = u32x4{0, 0, 0, 0};
+      if (i + kVec <= len) v[u] = *reinterpret_cast<const u32x4_any*>(p + i * (BF16 ? 2 : 4));
+    }
+#pragma unroll
+    for (int u = 0; u < kGradVecs; ++u) acc += squares<BF16>(v[u]);
+    const int rest = static_cast<int>(len % kVec);  // values behind the last whole vector
+    if (static_cast<int>(threadIdx.x) < rest) {
+      const int64_t i = len - rest + threadIdx.x;
+      acc += square(BF16 ? bf16_lo(reinterpret_cast<const uint16_t*>(p)[i]) : reinterpret_cast<const float*>(p)[i]);
+    }
+  }
+  const double s = block_sum_f64(acc);
+  if (threadIdx.x == 0) partial[blockIdx.x] = s;
+}
+
+__global__ __launch_bounds__(kGradThreads) void grad_total_kernel(const double* __restrict__ partial, int32_t m,
+                                                                  double* __restrict__ sumsq, bool accumulate) {
+  double acc = 0.0;
+  for (int32_t i = threadIdx.x; i < m; i += kGradThreads) acc += partial[i];
+  const double s = block_sum_f64(acc);
+  if (threadIdx.x == 0) *sumsq = accumulate ? *sumsq + s : s;
+}
+
+template <bool BF16>
+__global__ __launch_bounds__(kGradThreads) void grad_clip_kernel(const void* const* __restrict__ tensors,
+                                                                 const int64_t* __restrict__ numels, int32_t n,
+                                                                 const double* __restrict__ sumsq, double max_norm,
+                                                                 float* __restrict__ norm_out, void* const* __restrict__ out) {
+  extern __shared__ int64_t s_first[];
+  constexpr int kVec = BF16 ? 8 : 4, kChunk = kGradBytes / (BF16 ? 2 : 4), kSize = BF16 ? 2 : 4;
+  const double norm = sqrt(*sumsq), ratio = max_norm / (norm + 1e-6);
+  const double coef = ratio >= 1.0 ? 1.0 : ratio;  // NaN stays NaN; fp64, since a huge norm's factor is below fp32's range
+  if (blockIdx.x == 0 && threadIdx.x == 0 && norm_out != nullptr) *norm_out = static_cast<float>(norm);
+  if (coef == 1.0 && out == nullptr) return;
+  const Share sh = grad_share(tensors, numels, n, kChunk, s_first);
+  int32_t t = sh.tensor;
+  for (int64_t c = sh.begin; c < sh.end; ++c) {
+    while (t + 1 < n && s_first[t + 1] <= c) ++t;
+    const int64_t at = (c - s_first[t]) * kChunk, len = min(numels[t] - at, static_cast<int64_t>(kChunk));
+    const char* p = static_cast<const char*>(tensors[t]) + at * kSize;
+    void* to = out == nullptr ? nullptr : out[t];
+    char* d = to == nullptr ? const_cast<char*>(p) : static_cast<char*>(to) + at * kSize;
+    if (coef == 1.0 && d == p) continue;
+    u32x4 v[kGradVecs];
+#pragma unroll
+    for (int u = 0; u < kGradVecs; ++u) {
+      const int i = (u * kGradThreads + static_cast<int>(threadIdx.x)) * kVec;
+      if (i + kVec <= len) v[u] = *reinterpret_cast<const u32x4_any*>(p + i * kSize);
+    }
+#pragma unroll
+    for (int u = 0; u < kGradVecs; ++u) {
+      const int i = (u * kGradThreads + static_cast<int>(threadIdx.x)) * kVec;
+      if (i + kVec > len) continue;
+      u32x4 y;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        y[j] = BF16 ? pack_bf16(scaled(coef, bf16_lo(v[u][j])), scaled(coef, bf16_hi(v[u][j])))
+                    : bits_of(scaled(coef, f32_of(v[u][j])));
+      *reinterpret_cast<u32x4_any*>(d + i * kSize) = y;
+    }
+    const int rest = static_cast<int>(len % kVec);
+    if (static_cast<int>(threadIdx.x) < rest) {
+      const int64_t i = len - rest + threadIdx.x;
+      if (BF16)
+        reinterpret_cast<uint16_t*>(d)[i] =
+            static_cast<uint16_t>(pack_bf16(scaled(coef, bf16_lo(reinterpret_cast<const uint16_t*>(p)[i])), 0.f));
+      else
+        reinterpret_cast<float*>(d)[i] = scaled(coef, reinterpret_cast<const float*>(p)[i]);
+    }
+  }
+}
+
+}  // namespace
+
+hipError_t launch_grad_sumsq(const void* const* tensors, const int64_t* numels, int32_t n, bool bf16,
+                             double* sumsq, bool accumulate, double* partial, hipStream_t st) {
+  const int32_t grid = n > 0 ? kGradBlocks : 0;
+  if (grid > 0) {
+    if (bf16)
+      hipLaunchKernelGGL(grad_sumsq_kernel<true>, dim3(grid), dim3(kGradThreads), n * sizeof(int64_t), st, tensors, numels, n, partial);
+    else
+      hipLaunchKernelGGL(grad_sumsq_kernel<false>, dim3(grid), dim3(kGradThreads), n * sizeof(int64_t), st, tensors, numels, n, partial);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(grad_total_kernel, dim3(1), dim3(kGradThreads), 0, st, partial, grid, sumsq, accumulate);
+  return hipGetLastError();
+}
+
+hipError_t launch_grad_clip(const void* const* tensors, const int64_t* numels, int32_t n, bool bf16,
+                            const double* sumsq, double max_norm, float* norm, void* const* out,
+                            hipStream_t st) {
+  const int32_t grid = n > 0 ? kGradBlocks : 1;
+  if (bf16)
+    hipLaunchKernelGGL(grad_clip_kernel<true>, dim3(grid), dim3(kGradThreads), n * sizeof(int64_t), st, tensors, numels, n, sumsq, max_norm, norm, out);
+  else
+    hipLaunchKernelGGL(grad_clip_kernel<false>, dim3(grid), dim3(kGradThreads), n * sizeof(int64_t), st, tensors, numels, n, sumsq, max_norm, norm, out);
+  return hipGetLastError();
+}
+
+}  // namespace ultraep

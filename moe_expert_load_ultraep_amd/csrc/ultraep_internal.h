@@ -30,6 +30,10 @@ struct Shape {
   PlanLayout lay;
 };
 
+// Argument checks and status of the entry points.
+inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+inline int from_hip(hipError_t e) { return e == hipSuccess ? ULTRAEP_OK : ULTRAEP_ELAUNCH; }
+
 // Launchers.  All work is queued on `st`; none of them synchronises.
 // ws: 2*L*ntiles*E int32 (tile histograms, tile ordinal bases); TK = T*k
 // pairs per rank, N = R*TK per layer.  With inv non-null the dispatch
@@ -68,4 +72,33 @@ hipError_t launch_weight_sync(const Shape& sh, const int32_t* plan, const uint16
 size_t plan_lds_bytes(const Shape& sh);
 size_t rerouting_lds_bytes(const Shape& sh, bool layout);
 
+// The experts' steps (include/ultraep_experts.h).  off: the plan's PHYS_OFF
+// words from p_begin on, ne: experts of the range, cap: rows that are there.
+hipError_t launch_permute_quant(const int32_t* off, int32_t ne, const int32_t* inv, int32_t k,
+                                const uint16_t* hidden, int64_t hidden_rows, int32_t H, uint8_t* q,
+                                uint8_t* q_scale, uint8_t* qt, uint8_t* qt_scale, int64_t cap,
+                                hipStream_t st);
+hipError_t launch_weight_quant(const uint16_t* const* weights, int32_t n, int32_t N, int32_t K,
+                               uint8_t* q, uint8_t* q_scale, uint8_t* qt, uint8_t* qt_scale,
+                               hipStream_t st);
+hipError_t launch_expert_gemm(const int32_t* off, int32_t ne, const uint8_t* q,
+                              const uint8_t* q_scale, int32_t K, const uint8_t* const* w,
+                              const uint8_t* const* w_scale, int32_t N, uint16_t* out, int64_t cap,
+                              hipStream_t st);
+hipError_t launch_expert_wgrad(const int32_t* off, int32_t ne, const uint8_t* dyt,
+                               const uint8_t* dyt_scale, int32_t N, const uint8_t* xt,
+                               const uint8_t* xt_scale, int32_t K, int64_t cap, float* const* grads,
+                               bool accumulate, hipStream_t st);
+hipError_t launch_grad_sumsq(const void* const* tensors, const int64_t* numels, int32_t n,
+                             bool bf16, double* sumsq, bool accumulate, double* partial,
+                             hipStream_t st);
+hipError_t launch_grad_clip(const void* const* tensors, const int64_t* numels, int32_t n, bool bf16,
+                            const double* sumsq, double max_norm, float* norm, void* const* out,
+                            hipStream_t st);
+
 }  // namespace ultraep
+
+// The context behind the C ABI.
+struct ultraep_ctx {
+  ultraep::Shape sh;
+};
