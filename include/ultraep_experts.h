@@ -114,8 +114,9 @@ int ultraep_weight_quant(const ultraep_ctx* ctx, const uint16_t* const* weights,
  * With the gradient rows for q (K = the forward's N) and the transposed weights
  * this is the gradient of the forward's rows.
  * Errors: EINVAL (null pointers, N <= 0, K <= 0, bad range, capacity_rows < 0);
- *      EUNSUPPORTED (N % 8 != 0, N or K > 2^20, capacity_rows >= 2^31, q or out
- *      not 16-byte, q_scale not 4-byte, the tables not 8-byte aligned). */
+ *      EUNSUPPORTED (N % 8 != 0, N or K > 2^20, capacity_rows >= 2^31, more than
+ *      2^23 tiles of 256 x 256 with one to spare an expert, q or out not
+ *      16-byte, q_scale not 4-byte, the tables not 8-byte aligned). */
 int ultraep_expert_gemm(const ultraep_ctx* ctx, const void* plan, const uint8_t* q,
                         const uint8_t* q_scale, int32_t K, const uint8_t* const* w,
                         const uint8_t* const* w_scale, int32_t N, int32_t p_begin, int32_t p_end,

@@ -16,6 +16,12 @@ constexpr int32_t kMaxWidth = 1 << 20;        // N and K of the products
 constexpr int32_t kMaxRowWidth = 1 << 24;     // H of the quantiser
 constexpr int64_t kMaxRows = int64_t{1} << 31;
 
+constexpr int64_t kMaxTiles = 1 << 23;        // workgroups of a product
+
+bool too_many_tiles(int64_t rows, int32_t groups, int32_t width) {
+  return (rows / 256 + groups) * ((width + 255) / 256) > kMaxTiles;
+}
+
 bool bad_range(const ultraep_ctx* ctx, int32_t p_begin, int32_t p_end) {
   return p_begin < 0 || p_end < p_begin || p_end > ctx->sh.P;
 }
@@ -68,7 +74,8 @@ int ultraep_expert_gemm(const ultraep_ctx* ctx, const void* plan, const uint8_t*
   if (!ctx || !plan || !q || !q_scale || !w || !w_scale || !out) return ULTRAEP_EINVAL;
   if (N <= 0 || K <= 0 || capacity_rows < 0 || bad_range(ctx, p_begin, p_end)) return ULTRAEP_EINVAL;
   if (N % 8 != 0 || N > kMaxWidth || K > kMaxWidth || capacity_rows >= kMaxRows || !aligned(plan, 4) ||
-      !aligned(q, 16) || !aligned(q_scale, 4) || !aligned(w, 8) || !aligned(w_scale, 8) || !aligned(out, 16))
+      !aligned(q, 16) || !aligned(q_scale, 4) || !aligned(w, 8) || !aligned(w_scale, 8) || !aligned(out, 16) ||
+      too_many_tiles(capacity_rows, p_end - p_begin, N))
     return ULTRAEP_EUNSUPPORTED;
   return from_hip(ultraep::launch_expert_gemm(segment(ctx, plan, p_begin), p_end - p_begin, q, q_scale, K, w,
                                               w_scale, N, out, capacity_rows,

@@ -45,6 +45,49 @@ __device__ __forceinline__ int32_t find_group(const int32_t* off, int32_t ne, in
   return __builtin_amdgcn_readfirstlane(n - 1);
 }
 
+// The row tiles of a segment: each expert's rows in tiles of `unit`, no tile
+// without rows.  The counts are added up by a wave scan, 64 experts at a time;
+// every wave finds its tile by itself.  Every lane must be active; results are
+// wave-uniform.
+__device__ __forceinline__ int32_t tiles_upto(const int32_t* off, int32_t ne, int64_t cap, int32_t unit, int32_t p0) {
+  const int32_t p = p0 + lane_id();
+  const int32_t rows = p < ne ? group_row(off, p + 1, cap) - group_row(off, p, cap) : 0;
+  return wave_inclusive_scan((max(rows, 0) + unit - 1) / unit);
+}
+
+__device__ __forceinline__ int32_t row_tiles(const int32_t* off, int32_t ne, int64_t cap, int32_t unit) {
+  int32_t total = 0;
+  for (int32_t p0 = 0; p0 < ne; p0 += 64)
+    total += static_cast<int32_t>(readlane(static_cast<uint32_t>(tiles_upto(off, ne, cap, unit, p0)), 63));
+  return total;
+}
+
+struct RowTile {
+  int32_t p;     // expert
+  int64_t row0;  // first row, of the segment
+  int32_t rows;  // 1..unit
+};
+
+// Row tile m < row_tiles(...).
+__device__ __forceinline__ RowTile find_row_tile(const int32_t* off, int32_t ne, int64_t cap, int32_t unit, int32_t m) {
+  int32_t before = 0;
+  for (int32_t p0 = 0;; p0 += 64) {
+    const int32_t upto = tiles_upto(off, ne, cap, unit, p0);
+    const int32_t all = static_cast<int32_t>(readlane(static_cast<uint32_t>(upto), 63));
+    if (m - before >= all && p0 + 64 < ne) {
+      before += all;
+      continue;
+    }
+    const int32_t l = min(static_cast<int32_t>(__builtin_popcountll(ballot(upto <= m - before))), 63);
+    const int32_t p = p0 + l;
+    const int32_t first = l > 0 ? static_cast<int32_t>(readlane(static_cast<uint32_t>(upto), max(l - 1, 0))) : 0;
+    const int32_t o0 = __builtin_amdgcn_readfirstlane(group_row(off, p, cap));
+    const int32_t o1 = __builtin_amdgcn_readfirstlane(group_row(off, p + 1, cap));
+    const int64_t row0 = o0 + static_cast<int64_t>(m - before - first) * unit;
+    return RowTile{p, row0, static_cast<int32_t>(min(o1 - row0, static_cast<int64_t>(unit)))};
+  }
+}
+
 // Exponent of a block whose largest finite magnitude has these float bits:
 // the smallest e >= -126 with amax <= 448 * 2^e = 1.75 * 2^(8 + e), 0 for a
 // block without a finite value other than zero.

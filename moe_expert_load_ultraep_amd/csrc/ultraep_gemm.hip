@@ -175,6 +175,324 @@ __global__ __launch_bounds__(kMmThreads) void expert_gemm_kernel(
   }
 }
 
+// Order of the tiles.  Workgroups go to the eight XCDs in turn; each XCD takes
+// one contiguous eighth of a walk that goes through eight row tiles by all
+// column tiles at a time, so that the workgroups that share an L2 at one time
+// read a near-square set of rows and weights.
+struct Tile2 {
+  int32_t m, n;
+};
+
+__device__ __forceinline__ Tile2 tile_order(int64_t t, int64_t tiles, int32_t mtile, int32_t ntile) {
+  constexpr int kGroup = 8;
+  const int64_t full = tiles & ~int64_t{7};
+  if (t < full) t = (t & 7) * (full >> 3) + (t >> 3);
+  const int64_t per = static_cast<int64_t>(kGroup) * ntile;
+  const int32_t g = static_cast<int32_t>(t / per);
+  const int32_t r = static_cast<int32_t>(t - g * per);
+  const int32_t width = min(kGroup, mtile - g * kGroup);
+  return Tile2{g * kGroup + r % width, r / width};
+}
+
+// ------------------------------------------------------------------------
+// The 256 x 256 tile
+// ------------------------------------------------------------------------
+typedef __attribute__((address_space(3))) uint8_t lds_u8;
+typedef __attribute__((address_space(1))) int global_int;
+
+constexpr int kBigTile = 256;        // rows of either operand
+constexpr int kHalfBytes = 128 * 128;  // half of an operand's block of 128, in LDS
+
+// One operand of a tile: row r of block b at base + min(r, last) * row_pitch +
+// b * block_pitch, 128 bytes.
+struct BigOperand {
+  const uint8_t* base;
+  int64_t block_pitch;
+  uint32_t row_pitch;
+  int32_t last;
+};
+
+// A wave's 128 rows of A are read as 16-row fragments i = 0..7, fragment row m
+// being row 32 * (m / 4) + 4 * i + m % 4, so that a lane's accumulators
+// (fragment rows 4 * (l / 16) + r) are 32 consecutive rows: whole lines when
+// they are stored.  B's fragment j holds rows 16 * j + m.
+//
+// Half H of an operand's block is what the two waves along it read as
+// fragments 4H..4H+3, 64 rows each: row s of the half is this row of the tile.
+template <bool A, int H>
+__device__ __forceinline__ int half_row(int s) {
+  return A ? 128 * (s >> 6) + 32 * ((s >> 4) & 3) + 16 * H + (s & 15) : 128 * (s >> 6) + 64 * H + (s & 63);
+}
+
+// In LDS a row is eight 16-byte parts, part c at c ^ key(row): the key differs
+// among eight lanes that read one part of their rows together, so they meet
+// different banks.
+template <bool A>
+__device__ __forceinline__ int part_key(int s) {
+  return A ? (s & 3) | (((s >> 4) & 1) << 2) : s & 7;
+}
+
+// Byte offsets of the four 16-byte parts that this lane loads of half H.
+template <bool A, int H>
+__device__ __forceinline__ void load_offsets(const BigOperand& op, uint32_t (&off)[4]) {
+  const int lane = lane_id(), wv = threadIdx.x >> 6;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int s = wv * 32 + u * 8 + (lane >> 3);
+    off[u] = static_cast<uint32_t>(min(half_row<A, H>(s), op.last)) * op.row_pitch +
+             static_cast<uint32_t>(((lane & 7) ^ part_key<A>(s)) * 16);
+  }
+}
+
+// Half a block of an operand into LDS, asynchronously: four loads a wave, 1 KiB
+// (eight rows) each.  At and behind `blocks` the resource is empty and zeros
+// arrive, so the loop over blocks has no branches.
+struct HalfLoad {
+  __amdgpu_buffer_rsrc_t src;
+  lds_u8* dst;
+  const uint32_t (&off)[4];
+
+  __device__ __forceinline__ HalfLoad(const BigOperand& op, int32_t b, int32_t blocks, const uint32_t (&o)[4], uint8_t* lds)
+      : src(row_rsrc(op.base + min(b, blocks - 1) * op.block_pitch, b < blocks ? 0x7FFFFFFFu : 0u)),
+        dst((lds_u8*)lds + __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6)) * 4096),
+        off(o) {}
+
+  __device__ __forceinline__ void issue(int u) const {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(src, dst + u * 1024, 16, static_cast<int>(off[u]), 0, 0, 0);
+  }
+};
+
+__device__ __forceinline__ void load_half(const BigOperand& op, int32_t b, int32_t blocks, const uint32_t (&off)[4],
+                                          uint8_t* lds) {
+  const HalfLoad load(op, b, blocks, off, lds);
+#pragma unroll
+  for (int u = 0; u < 4; ++u) load.issue(u);
+}
+
+// Every wave's LDS reads are done and all but its last LOADS loads have
+// arrived; then the workgroup meets.
+template <int LOADS>
+__device__ __forceinline__ void meet() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((LOADS & 15) | (7 << 4) | ((LOADS >> 4) << 14));
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// acc += A B of one 16 x 16 x 128 with byte BYTE of the scale words.  Written as
+// volatile asm for two reasons: the accumulator is updated where it is (with
+// the builtin the compiler picks another destination and moves whole
+// accumulators about, 460 moves in 256 products), and products and LDS reads
+// stay in the order of the source.  The s_nop covers a scale word or fragment
+// that a vector instruction wrote just before.
+template <int BYTE>
+__device__ __forceinline__ void product(f32x4& acc, const i32x8& a, const i32x8& b, int xa, int xb) {
+  if constexpr (BYTE == 0)
+    asm volatile("s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[0,0,0] op_sel_hi:[0,0,0]"
+                 : "+a"(acc) : "v"(a), "v"(b), "v"(xa), "v"(xb));
+  else if constexpr (BYTE == 1)
+    asm volatile("s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[1,1,0] op_sel_hi:[0,0,0]"
+                 : "+a"(acc) : "v"(a), "v"(b), "v"(xa), "v"(xb));
+  else if constexpr (BYTE == 2)
+    asm volatile("s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[0,0,0] op_sel_hi:[1,1,0]"
+                 : "+a"(acc) : "v"(a), "v"(b), "v"(xa), "v"(xb));
+  else
+    asm volatile("s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[1,1,0] op_sel_hi:[1,1,0]"
+                 : "+a"(acc) : "v"(a), "v"(b), "v"(xa), "v"(xb));
+}
+
+// Behind the products: their results are there before a vector instruction, a
+// copy the compiler makes included, reads them (19 wait states).  It stands in
+// the loop's own block, since copies start where the loop ends.
+__device__ __forceinline__ void products_done() { asm volatile("s_nop 15\n\ts_nop 3"); }
+
+// Fragment i of a half in LDS; at[h]: this lane's part h.
+template <int STRIDE>
+__device__ __forceinline__ i32x8 read_fragment(const uint8_t* lds, const int (&at)[2], int i) {
+  return __builtin_shufflevector(*reinterpret_cast<const i32x4*>(lds + at[0] + i * STRIDE),
+                                 *reinterpret_cast<const i32x4*>(lds + at[1] + i * STRIDE), 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+constexpr int kStrideA = 4 * 128, kStrideB = 16 * 128;  // bytes from a fragment's rows to the next one's
+
+// A quarter of the wave's products: fragments a[4] by b[4], with the reads of
+// the four fragments f of half `lds` and the loads of another half among them: a
+// load's issue takes long enough for the matrix unit to run dry when several
+// follow each other.
+template <int I0, int J0, int BYTE, int STRIDE>
+__device__ __forceinline__ void quadrant(const i32x8 (&a)[4], const i32x8 (&b)[4], int xa, const int (&xb)[8],
+                                         f32x4 (&acc)[8][8], const uint8_t* lds, const int (&at)[2], i32x8 (&f)[4], const HalfLoad& load) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      product<BYTE>(acc[I0 + i][J0 + j], a[i], b[j], xa, xb[J0 + j]);
+      if (j == 0) f[i] = read_fragment<STRIDE>(lds, at, i);
+      if (j == 2) load.issue(i);
+    }
+}
+
+// Scale bytes of four blocks: one word for the wave's 128 rows of A, one a
+// fragment row of B.
+struct ScaleWords {
+  int a;
+  int b[8];
+};
+
+struct ScaleSource {
+  const uint8_t* a;  // the wave's row of weight scales
+  const uint8_t* b;  // the tile's first row of row scales
+  int32_t pitch;     // bytes a row
+  int32_t last;      // B's last row
+};
+
+__device__ __forceinline__ void load_scales(const ScaleSource& s, int32_t block, ScaleWords& w) {
+  const int row0 = ((threadIdx.x >> 6) & 1) * 128 + (lane_id() & 15);
+  w.a = *reinterpret_cast<const global_int*>(reinterpret_cast<uintptr_t>(s.a) + block);
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    w.b[j] = *reinterpret_cast<const int*>(s.b + static_cast<uint32_t>(min(row0 + 16 * j, s.last)) * s.pitch + block);
+}
+
+// Waits for the words here, and not at their first use in the loop.
+__device__ __forceinline__ void settle(ScaleWords& w) {
+  asm volatile("" : "+v"(w.a));
+#pragma unroll
+  for (int j = 0; j < 8; ++j) asm volatile("" : "+v"(w.b[j]));
+}
+
+// LDS and registers of the pipeline.  Halves are indexed [block parity][half].
+struct Offsets {
+  uint32_t a[2][4], b[2][4];
+  int read_a[2], read_b[2];
+};
+
+// One block of 128, the U-th of four: the wave's 8 x 8 products of 16 x 16 x 128
+// in four quadrants, odd blocks walking B's halves the other way round.  Every
+// half is read once, in the quadrant before its first use, and the barrier
+// behind that quadrant frees it for the block after next: its loads have seven
+// quadrants (about 3600 cycles of products) to arrive, and 112 of the 128 KiB
+// are in flight or waiting at any time.
+template <int U>
+__device__ __forceinline__ void big_step(const BigOperand& a, const BigOperand& b, const Offsets& o, int32_t k,
+                                         int32_t blocks, uint8_t* alo, uint8_t* ahi, uint8_t* bx, uint8_t* by,
+                                         uint8_t* next_alo, uint8_t* next_by, i32x8 (&fal)[4], i32x8 (&fah)[4],
+                                         i32x8 (&fbx)[4], i32x8 (&fby)[4], const ScaleSource& ss, ScaleWords& sw,
+                                         ScaleWords& sn, f32x4 (&acc)[8][8]) {
+  constexpr int X = U & 1, Y = 1 - X;
+  meet<16>();
+  quadrant<0, 4 * X, U, kStrideB>(fal, fbx, sw.a, sw.b, acc, by, o.read_b, fby, HalfLoad(a, k + 2, blocks, o.a[0], alo));
+  quadrant<0, 4 * Y, U, kStrideA>(fal, fby, sw.a, sw.b, acc, ahi, o.read_a, fah, HalfLoad(b, k + 2, blocks, o.b[X], bx));
+  meet<16>();
+  if (U == 2) load_scales(ss, min(k + 2, blocks - 1) & ~3, sn);
+  quadrant<4, 4 * Y, U, kStrideA>(fah, fby, sw.a, sw.b, acc, next_alo, o.read_a, fal,
+                                  HalfLoad(b, k + 2, blocks, o.b[Y], by));
+  quadrant<4, 4 * X, U, kStrideB>(fah, fbx, sw.a, sw.b, acc, next_by, o.read_b, fby,
+                                  HalfLoad(a, k + 2, blocks, o.a[1], ahi));
+  if (U == 3) {
+    sw = sn;
+    products_done();
+  }
+}
+
+// What the products of one segment share.
+struct GemmArgs {
+  const int32_t* off;
+  int32_t ne;
+  const uint8_t* q;
+  const uint8_t* q_scale;
+  int32_t K;
+  const uint8_t* const* w;
+  const uint8_t* const* w_scale;
+  int32_t N;
+  uint16_t* out;
+  int64_t cap;
+};
+
+// Whether expert p's weights are there to be used.
+__device__ __forceinline__ bool usable(const uint8_t* w, const uint8_t* ws) {
+  return w != nullptr && ws != nullptr && (reinterpret_cast<uintptr_t>(w) & 15) == 0 &&
+         (reinterpret_cast<uintptr_t>(ws) & 3) == 0;
+}
+
+// out[row][n]: A is the weights (a lane holds 32 consecutive n of a row), B the
+// rows; one 256 x 256 tile a workgroup, four waves of 128 x 128.
+__global__ __launch_bounds__(kMmThreads, 1) void expert_gemm_big_kernel(GemmArgs g, int32_t ntile) {
+  __shared__ __align__(16) uint8_t a00[kHalfBytes], a01[kHalfBytes], a10[kHalfBytes], a11[kHalfBytes];
+  __shared__ __align__(16) uint8_t b00[kHalfBytes], b01[kHalfBytes], b10[kHalfBytes], b11[kHalfBytes];
+  const int32_t Kp = q_pitch(g.K), Ks = s_pitch(g.K), blocks = Kp / 128;
+  const int lane = lane_id(), l16 = lane & 15, kg = lane >> 4;
+  const int wv = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6)), wi = wv >> 1, wj = wv & 1;
+  const int32_t mtile = row_tiles(g.off, g.ne, g.cap, kBigTile);
+  const int64_t tiles = static_cast<int64_t>(mtile) * ntile;
+  if (blockIdx.x >= tiles) return;
+  const Tile2 at = tile_order(blockIdx.x, tiles, mtile, ntile);
+  const RowTile rt = find_row_tile(g.off, g.ne, g.cap, kBigTile, at.m);
+  const uint8_t* wp = g.w[rt.p];
+  const uint8_t* ws = g.w_scale[rt.p];
+  if (!usable(wp, ws)) return;
+  const int32_t n0 = at.n * kBigTile, rows = rt.rows, cols = min(g.N - n0, kBigTile);
+  const BigOperand a{wp + static_cast<int64_t>(n0) * Kp, 128, static_cast<uint32_t>(Kp), cols - 1};
+  const BigOperand b{g.q + rt.row0 * Kp, 128, static_cast<uint32_t>(Kp), rows - 1};
+  const int32_t sblock = min(n0 / 128 + wi, ceil_div(g.N, 128) - 1);
+  const ScaleSource ss{ws + static_cast<int64_t>(sblock) * Ks, g.q_scale + rt.row0 * Ks, Ks, rows - 1};
+  Offsets o;
+  load_offsets<true, 0>(a, o.a[0]);
+  load_offsets<true, 1>(a, o.a[1]);
+  load_offsets<false, 0>(b, o.b[0]);
+  load_offsets<false, 1>(b, o.b[1]);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int part = ((2 * kg + h) ^ (l16 & 7)) * 16;
+    o.read_a[h] = (wi * 64 + 16 * (l16 >> 2) + (l16 & 3)) * 128 + part;
+    o.read_b[h] = (wj * 64 + l16) * 128 + part;
+  }
+  ScaleWords sw, sn;
+  load_scales(ss, 0, sw);
+  settle(sw);
+  load_half(a, 0, blocks, o.a[0], a00);
+  load_half(b, 0, blocks, o.b[0], b00);
+  load_half(b, 0, blocks, o.b[1], b01);
+  load_half(a, 0, blocks, o.a[1], a01);
+  load_half(a, 1, blocks, o.a[0], a10);
+  load_half(b, 1, blocks, o.b[1], b11);
+  load_half(b, 1, blocks, o.b[0], b10);
+  load_half(a, 1, blocks, o.a[1], a11);
+  f32x4 acc[8][8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  i32x8 fal[4], fah[4], fb0[4], fb1[4];
+  meet<24>();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    fal[i] = read_fragment<kStrideA>(a00, o.read_a, i);
+    fb0[i] = read_fragment<kStrideB>(b00, o.read_b, i);
+  }
+  for (int32_t k = 0; k < blocks; k += 4) {
+    big_step<0>(a, b, o, k, blocks, a00, a01, b00, b01, a10, b11, fal, fah, fb0, fb1, ss, sw, sn, acc);
+    big_step<1>(a, b, o, k + 1, blocks, a10, a11, b11, b10, a00, b00, fal, fah, fb1, fb0, ss, sw, sn, acc);
+    big_step<2>(a, b, o, k + 2, blocks, a00, a01, b00, b01, a10, b11, fal, fah, fb0, fb1, ss, sw, sn, acc);
+    big_step<3>(a, b, o, k + 3, blocks, a10, a11, b11, b10, a00, b00, fal, fah, fb1, fb0, ss, sw, sn, acc);
+  }
+  const int c = wi * 128 + 32 * kg;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int r = wj * 128 + 16 * j + l16;
+    if (r < rows) {
+      u32x4* d = reinterpret_cast<u32x4*>(g.out + (rt.row0 + r) * g.N + n0 + c);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (c + 8 * i < cols)
+          d[i] = u32x4{pack_bf16(acc[2 * i][j][0], acc[2 * i][j][1]), pack_bf16(acc[2 * i][j][2], acc[2 * i][j][3]),
+                       pack_bf16(acc[2 * i + 1][j][0], acc[2 * i + 1][j][1]),
+                       pack_bf16(acc[2 * i + 1][j][2], acc[2 * i + 1][j][3])};
+    }
+  }
+  meet<0>();  // no load outlives the workgroup's LDS
+}
+
 // grads[p][n][k]: A is x (four consecutive k a lane), B is dy.
 __global__ __launch_bounds__(kMmThreads) void expert_wgrad_kernel(
     const int32_t* __restrict__ off, int32_t ne, const uint8_t* __restrict__ dyt, const uint8_t* __restrict__ dyt_scale,
@@ -227,6 +545,13 @@ hipError_t launch_expert_gemm(const int32_t* off, int32_t ne, const uint8_t* q, 
                               const uint8_t* const* w, const uint8_t* const* w_scale, int32_t N, uint16_t* out,
                               int64_t cap, hipStream_t st) {
   if (ne == 0 || cap == 0) return hipSuccess;
+  if (cap / ne >= 64) {
+    const int32_t ntile = ceil_div(N, kBigTile), mtile = static_cast<int32_t>(cap / kBigTile) + ne;
+    const GemmArgs g{off, ne, q, q_scale, K, w, w_scale, N, out, cap};
+    hipLaunchKernelGGL(expert_gemm_big_kernel, dim3(static_cast<uint32_t>(static_cast<int64_t>(mtile) * ntile)),
+                       dim3(kMmThreads), 0, st, g, ntile);
+    return hipGetLastError();
+  }
   const int32_t ntile = ceil_div(N, kMmTile);
   const int64_t tiles = (cap / kMmTile + ne) * ntile;
   hipLaunchKernelGGL(expert_gemm_kernel, dim3(mm_grid(tiles)), dim3(kMmThreads), 0, st, off, ne, q, q_scale, K, w,

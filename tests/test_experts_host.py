@@ -76,7 +76,7 @@ def test_expert_gemm_refusals(ctx):
                 dict(K=0), dict(N=0), dict(cap=-1), dict(p0=-1), dict(p0=4), dict(p1=13)):
         assert call(**bad) == -1, bad
     for bad in (dict(N=12), dict(K=(1 << 20) + 8), dict(q=F + 8), dict(qs=F + 1), dict(w=F + 4), dict(ws=F + 4),
-                dict(out=F + 8), dict(cap=1 << 31)):
+                dict(out=F + 8), dict(cap=1 << 31), dict(cap=1 << 30, N=1 << 20)):
         assert call(**bad) == -2, bad
     assert call(cap=0) == 0 and call(p0=2, p1=2) == 0
 
