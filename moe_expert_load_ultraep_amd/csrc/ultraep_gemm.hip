@@ -224,12 +224,12 @@ __device__ __forceinline__ int half_row(int s) {
   return A ? 128 * (s >> 6) + 32 * ((s >> 4) & 3) + 16 * H + (s & 15) : 128 * (s >> 6) + 64 * H + (s & 63);
 }
 
-// In LDS a row is eight 16-byte parts, part c at c ^ key(row): the key differs
-// among eight lanes that read one part of their rows together, so they meet
-// different banks.
+// In LDS a row is eight 16-byte parts, part c at c ^ key(row).  64 banks are two
+// rows wide: an even and an odd row share a key, and the eight pairs of the
+// sixteen rows that are read together have different ones.
 template <bool A>
 __device__ __forceinline__ int part_key(int s) {
-  return A ? (s & 3) | (((s >> 4) & 1) << 2) : s & 7;
+  return A ? ((s >> 1) & 1) | (((s >> 4) & 3) << 1) : (s >> 1) & 7;
 }
 
 // Byte offsets of the four 16-byte parts that this lane loads of half H.
@@ -443,7 +443,7 @@ __global__ __launch_bounds__(kMmThreads, 1) void expert_gemm_big_kernel(GemmArgs
   load_offsets<false, 1>(b, o.b[1]);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const int part = ((2 * kg + h) ^ (l16 & 7)) * 16;
+    const int part = ((2 * kg + h) ^ (l16 >> 1)) * 16;
     o.read_a[h] = (wi * 64 + 16 * (l16 >> 2) + (l16 & 3)) * 128 + part;
     o.read_b[h] = (wj * 64 + l16) * 128 + part;
   }
@@ -488,6 +488,232 @@ __global__ __launch_bounds__(kMmThreads, 1) void expert_gemm_big_kernel(GemmArgs
           d[i] = u32x4{pack_bf16(acc[2 * i][j][0], acc[2 * i][j][1]), pack_bf16(acc[2 * i][j][2], acc[2 * i][j][3]),
                        pack_bf16(acc[2 * i + 1][j][0], acc[2 * i + 1][j][1]),
                        pack_bf16(acc[2 * i + 1][j][2], acc[2 * i + 1][j][3])};
+    }
+  }
+  meet<0>();  // no load outlives the workgroup's LDS
+}
+
+// ------------------------------------------------------------------------
+// The weight gradients' 256 x 256 tile
+// ------------------------------------------------------------------------
+typedef int i32x2v __attribute__((ext_vector_type(2)));
+
+// acc += A B of one 16 x 16 x 32 in bf16, in place (see product); nothing that
+// it reads is written by the two vector instructions before it.
+__device__ __forceinline__ void product_wide(f32x4& acc, const i32x4& a, const i32x4& b) {
+  asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
+}
+
+// Values 4 * HALF..4 * HALF + 3 of eight e4m3 bytes, times their scale, as bf16.
+template <int HALF>
+__device__ __forceinline__ void widen_half(i32x4& y, const i32x2v& raw, float scale) {
+  int lo, hi;
+  asm volatile("v_cvt_scalef32_pk_bf16_fp8 %0, %1, %2" : "=v"(lo) : "v"(raw[HALF]), "v"(scale));
+  asm volatile("v_cvt_scalef32_pk_bf16_fp8 %0, %1, %2 op_sel:[1,0,0]" : "=v"(hi) : "v"(raw[HALF]), "v"(scale));
+  y[2 * HALF] = lo;
+  y[2 * HALF + 1] = hi;
+}
+
+// A block of 128 is 32 steps n = 8 g + i: A's fragment i by B's eight, over the
+// g-th eight of each lane's 32 values.  During step n the fragment of A for step
+// n + 1 and fragment i of B for the next g are widened, an instruction or two
+// behind each product, from bytes read from LDS four steps before.
+struct WideState {
+  i32x4 a[2];     // A's fragment of this step and of the next
+  i32x4 b[2][8];  // B's of this g and of the next
+  i32x2v raw_a[4], raw_b[4];
+  float sa[8], sb[8];  // scales of the block being widened
+  int na[8], nb[8];    // scale bytes of the next one
+};
+
+struct WideTile {
+  BigOperand a, b;
+  const uint8_t *scale_a, *scale_b;  // scale bytes of the tile's rows, block 0
+  int32_t pitch_a, pitch_b;          // scale bytes a block
+  int32_t row_a, row_b;              // this lane's row of fragment 0
+  uint32_t off_a[2][4], off_b[2][4];
+  int at_a[4], at_b[4];              // LDS offset of this lane's eight bytes g, in a half
+};
+
+// Eight bytes of fragment i; the fragments' rows lie in two halves.
+template <int STRIDE>
+__device__ __forceinline__ i32x2v read_raw(const uint8_t* lo, const uint8_t* hi, int at, int i) {
+  return *reinterpret_cast<const i32x2v*>((i < 4 ? lo : hi) + at + (i & 3) * STRIDE);
+}
+
+__device__ __forceinline__ int scale_byte(const uint8_t* s, int32_t row, int32_t last) { return s[min(row, last)]; }
+
+// Block k in LDS buffers [half] of its parity; n_*: the other parity's, where
+// block k + 1 is or arrives.  B's halves are read up to step 19 and A's up to
+// step 26; behind the barriers there the loads of block k + 2 go into them, 32
+// steps (about 4100 cycles of products) before they are read.
+__device__ __forceinline__ void wide_block(const WideTile& t, WideState& w, int32_t k, int32_t blocks, uint8_t* al,
+                                           uint8_t* ah, uint8_t* bl, uint8_t* bh, uint8_t* nal, uint8_t* nah, uint8_t* nbl,
+                                           uint8_t* nbh, f32x4 (&acc)[8][8]) {
+  const HalfLoad load_al(t.a, k + 2, blocks, t.off_a[0], al), load_ah(t.a, k + 2, blocks, t.off_a[1], ah);
+  const HalfLoad load_bl(t.b, k + 2, blocks, t.off_b[0], bl), load_bh(t.b, k + 2, blocks, t.off_b[1], bh);
+  const int64_t next = min(k + 1, blocks - 1);
+  const uint8_t* sa = t.scale_a + next * t.pitch_a;
+  const uint8_t* sb = t.scale_b + next * t.pitch_b;
+#pragma unroll
+  for (int n = 0; n < 32; ++n) {
+    const int g = n >> 3, i = n & 7;
+    if (n == 20 || n == 27) meet<8>();
+    if (n == 24) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w.sb[j] = scale_of(w.nb[j]);
+    }
+    if (n == 31) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w.sa[j] = scale_of(w.na[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      product_wide(acc[i][j], w.a[n & 1], w.b[g & 1][j]);
+      if (j == 0) widen_half<0>(w.a[(n + 1) & 1], w.raw_a[(n + 1) & 3], w.sa[(n + 1) & 7]);
+      if (j == 1) widen_half<1>(w.a[(n + 1) & 1], w.raw_a[(n + 1) & 3], w.sa[(n + 1) & 7]);
+      if (j == 2) widen_half<0>(w.b[(g + 1) & 1][i], w.raw_b[n & 3], w.sb[i]);
+      if (j == 3) widen_half<1>(w.b[(g + 1) & 1][i], w.raw_b[n & 3], w.sb[i]);
+      if (j == 4) {
+        const int m = n + 5;
+        w.raw_a[m & 3] = m < 32 ? read_raw<kStrideA>(al, ah, t.at_a[(m >> 3) & 3], m & 7)
+                                : read_raw<kStrideA>(nal, nah, t.at_a[0], m & 7);
+      }
+      if (j == 5) {
+        const int m = n + 4;  // widened at step m for g + 1
+        w.raw_b[m & 3] = m < 24 ? read_raw<kStrideB>(bl, bh, t.at_b[((m >> 3) + 1) & 3], m & 7)
+                                : read_raw<kStrideB>(nbl, nbh, t.at_b[((m >> 3) + 1) & 3], m & 7);
+      }
+      if (j == 6 || j == 7) {
+        if (n >= 2 && n < 10) {
+          if (j == 6) w.na[n - 2] = scale_byte(sa, t.row_a + 4 * (n - 2), t.a.last);
+          if (j == 7) w.nb[n - 2] = scale_byte(sb, t.row_b + 16 * (n - 2), t.b.last);
+        }
+        if (n >= 20 && n < 24) (j == 6 ? load_bl : load_bh).issue(n - 20);
+        if (n >= 27 && n < 31) (j == 6 ? load_al : load_ah).issue(n - 27);
+      }
+    }
+  }
+}
+
+// The expert with the rank-th most rows (ties: lower expert first) of at most
+// 64; of more, the rank-th expert.
+__device__ __forceinline__ int32_t expert_of_rank(const int32_t* off, int32_t ne, int64_t cap, int32_t rank) {
+  if (ne > 64) return rank;
+  const int32_t l = lane_id(), p = min(l, ne - 1);
+  const int32_t rows = l < ne ? group_row(off, p + 1, cap) - group_row(off, p, cap) : -1;
+  int32_t before = 0;
+  for (int32_t q = 0; q < ne; ++q) {
+    const int32_t other = static_cast<int32_t>(readlane(static_cast<uint32_t>(rows), q));
+    before += other > rows || (other == rows && q < l) ? 1 : 0;
+  }
+  return __builtin_amdgcn_readfirstlane(lowest_lane(ballot(l < ne && before == rank)));
+}
+
+// grads[p][n][k]: A is x (a lane holds 32 consecutive k of a row n), B is dy.
+__global__ __launch_bounds__(kMmThreads, 1) void expert_wgrad_big_kernel(
+    const int32_t* off, int32_t ne, const uint8_t* dyt, const uint8_t* dyt_scale, int32_t N, const uint8_t* xt,
+    const uint8_t* xt_scale, int32_t K, int64_t cap, float* const* grads, bool accumulate, int32_t ntile,
+    int32_t ktile) {
+  __shared__ __align__(16) uint8_t a00[kHalfBytes], a01[kHalfBytes], a10[kHalfBytes], a11[kHalfBytes];
+  __shared__ __align__(16) uint8_t b00[kHalfBytes], b01[kHalfBytes], b10[kHalfBytes], b11[kHalfBytes];
+  const int lane = lane_id(), l16 = lane & 15, kg = lane >> 4;
+  const int wv = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6)), wi = wv >> 1, wj = wv & 1;
+  // every expert's tiles are dealt to all XCDs (experts differ in rows, so an
+  // XCD must not get whole ones), the expert with the most rows first
+  const int32_t per = ntile * ktile, turn = static_cast<int32_t>(blockIdx.x) / per;
+  const Tile2 at = tile_order(blockIdx.x - turn * per, per, ntile, ktile);
+  const int32_t p = expert_of_rank(off, ne, cap, turn), tn = at.m, tk = at.n;
+  float* out = grads[p];
+  if (out == nullptr) return;
+  const int32_t o0 = group_row(off, p, cap), o1 = group_row(off, p + 1, cap);
+  const int32_t blocks = max(ceil_div(o1 - o0, kQBlock), 0);
+  if (blocks == 0 && accumulate) return;
+  const int64_t first = o0 / kQBlock + p;
+  const int32_t n0 = tn * kBigTile, k0 = tk * kBigTile, rows = min(N - n0, kBigTile), cols = min(K - k0, kBigTile);
+  f32x4 acc[8][8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  if (blocks > 0) {
+    WideTile t;
+    t.a = BigOperand{xt + (first * K + k0) * kQBlock, static_cast<int64_t>(K) * kQBlock, 128u, cols - 1};
+    t.b = BigOperand{dyt + (first * N + n0) * kQBlock, static_cast<int64_t>(N) * kQBlock, 128u, rows - 1};
+    t.scale_a = xt_scale + first * K + k0;
+    t.scale_b = dyt_scale + first * N + n0;
+    t.pitch_a = K;
+    t.pitch_b = N;
+    t.row_a = wi * 128 + 32 * (l16 >> 2) + (l16 & 3);
+    t.row_b = wj * 128 + l16;
+    load_offsets<true, 0>(t.a, t.off_a[0]);
+    load_offsets<true, 1>(t.a, t.off_a[1]);
+    load_offsets<false, 0>(t.b, t.off_b[0]);
+    load_offsets<false, 1>(t.b, t.off_b[1]);
+    // odd lanes of sixteen take the two eights of a part the other way round, so
+    // that 32 lanes reading eight bytes meet all banks once
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int part = ((2 * kg + (g >> 1)) ^ (l16 >> 1)) * 16 + ((g ^ kg) & 1) * 8;
+      t.at_a[g] = (wi * 64 + 16 * (l16 >> 2) + (l16 & 3)) * 128 + part;
+      t.at_b[g] = (wj * 64 + l16) * 128 + part;
+    }
+    WideState w;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      w.sa[j] = scale_of(scale_byte(t.scale_a, t.row_a + 4 * j, t.a.last));
+      w.sb[j] = scale_of(scale_byte(t.scale_b, t.row_b + 16 * j, t.b.last));
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) asm volatile("" : "+v"(w.sa[j]), "+v"(w.sb[j]));
+    load_half(t.b, 0, blocks, t.off_b[0], b00);
+    load_half(t.b, 0, blocks, t.off_b[1], b01);
+    load_half(t.a, 0, blocks, t.off_a[0], a00);
+    load_half(t.a, 0, blocks, t.off_a[1], a01);
+    load_half(t.b, 1, blocks, t.off_b[0], b10);
+    load_half(t.b, 1, blocks, t.off_b[1], b11);
+    load_half(t.a, 1, blocks, t.off_a[0], a10);
+    load_half(t.a, 1, blocks, t.off_a[1], a11);
+    meet<16>();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const i32x2v raw = read_raw<kStrideB>(b00, b01, t.at_b[0], j);
+      widen_half<0>(w.b[0][j], raw, w.sb[j]);
+      widen_half<1>(w.b[0][j], raw, w.sb[j]);
+    }
+    const i32x2v raw = read_raw<kStrideA>(a00, a01, t.at_a[0], 0);
+    widen_half<0>(w.a[0], raw, w.sa[0]);
+    widen_half<1>(w.a[0], raw, w.sa[0]);
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      w.raw_a[(m + 1) & 3] = read_raw<kStrideA>(a00, a01, t.at_a[0], m + 1);
+      w.raw_b[m] = read_raw<kStrideB>(b00, b01, t.at_b[1], m);
+    }
+    asm volatile("s_nop 1");
+    for (int32_t k = 0; k < blocks; k += 2) {
+      wide_block(t, w, k, blocks, a00, a01, b00, b01, a10, a11, b10, b11, acc);
+      wide_block(t, w, k + 1, blocks, a10, a11, b10, b11, a00, a01, b00, b01, acc);
+      products_done();
+    }
+  }
+  const bool vec = (reinterpret_cast<uintptr_t>(out) & 15) == 0;
+  const int c = wi * 128 + 32 * kg;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int r = wj * 128 + 16 * j + l16;
+    if (r >= rows) continue;
+    float* d = out + static_cast<int64_t>(n0 + r) * K + k0 + c;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (c + 4 * i >= cols) continue;
+      f32x4 y = acc[i][j];
+      if (vec) {
+        if (accumulate) y += *reinterpret_cast<const f32x4*>(d + 4 * i);
+        *reinterpret_cast<f32x4*>(d + 4 * i) = y;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) d[4 * i + e] = accumulate ? d[4 * i + e] + y[e] : y[e];
+      }
     }
   }
   meet<0>();  // no load outlives the workgroup's LDS
@@ -563,6 +789,12 @@ hipError_t launch_expert_wgrad(const int32_t* off, int32_t ne, const uint8_t* dy
                                const uint8_t* xt, const uint8_t* xt_scale, int32_t K, int64_t cap, float* const* grads,
                                bool accumulate, hipStream_t st) {
   if (ne == 0) return hipSuccess;
+  if (true) {
+    const int32_t ntile = ceil_div(N, kBigTile), ktile = ceil_div(K, kBigTile);
+    hipLaunchKernelGGL(expert_wgrad_big_kernel, dim3(static_cast<uint32_t>(ne * ntile * ktile)), dim3(kMmThreads), 0, st,
+                       off, ne, dyt, dyt_scale, N, xt, xt_scale, K, cap, grads, accumulate, ntile, ktile);
+    return hipGetLastError();
+  }
   const int32_t ntile = ceil_div(N, kMmTile), ktile = ceil_div(K, kMmTile);
   const int64_t tiles = static_cast<int64_t>(ne) * ntile * ktile;
   hipLaunchKernelGGL(expert_wgrad_kernel, dim3(mm_grid(tiles)), dim3(kMmThreads), 0, st, off, ne, dyt, dyt_scale, N, xt,
