@@ -24,156 +24,10 @@ namespace ultraep {
 namespace {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kMmThreads = 256;
-constexpr int kMmTile = 128;  // both ways
-
-// One operand of a tile: 128 of its rows, row r at base + min(r, last) *
-// row_pitch + b * block_pitch; its scale byte at scale + (min(r, last) >>
-// row_shift) * scale_row + b * scale_block.
-struct Operand {
-  const uint8_t* base;
-  const uint8_t* scale;
-  int64_t row_pitch, block_pitch;
-  int64_t scale_row, scale_block;
-  int32_t last;
-  int32_t row_shift;
-};
-
-// acc[i][j] of a wave: its 64 rows of A by its 64 rows of B as 4 x 4 products
-// of 16 x 16.  LDS holds 128 bytes a row in eight 16-byte parts, part c at
-// c ^ (row % 8), so that 16 lanes reading one part of 16 rows meet no bank twice
-// more often than they must.
-__device__ __forceinline__ bf16x8 widen(const i32x8& v, int g, float s) {
-  bf16x8 y;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t w = static_cast<uint32_t>(v[2 * g + i / 2]);
-    const bf16x2 b = i % 2 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, true)
-                           : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, false);
-    y[2 * i] = b[0];
-    y[2 * i + 1] = b[1];
-  }
-  return y;
-}
 
 __device__ __forceinline__ float scale_of(int byte) { return __builtin_bit_cast(float, static_cast<uint32_t>(byte) << 23); }
-
-template <bool WIDE>
-__device__ __forceinline__ void mm_tile(const Operand& a, const Operand& b, int32_t blocks, uint8_t* sa, uint8_t* sb,
-                                        f32x4 (&acc)[4][4]) {
-  const int tid = threadIdx.x, lane = lane_id(), wv = tid >> 6, wi = wv >> 1, wj = wv & 1;
-  const int l16 = lane & 15, kg = lane >> 4;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int32_t blk = 0; blk < blocks; ++blk) {
-    u32x4 va[4], vb[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int x = tid + u * kMmThreads, r = x >> 3, c = x & 7;
-      va[u] = *reinterpret_cast<const u32x4*>(a.base + min(r, a.last) * a.row_pitch + blk * a.block_pitch + c * 16);
-      vb[u] = *reinterpret_cast<const u32x4*>(b.base + min(r, b.last) * b.row_pitch + blk * b.block_pitch + c * 16);
-    }
-    int xa[4], xb[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int ra = min(wi * 64 + i * 16 + l16, a.last), rb = min(wj * 64 + i * 16 + l16, b.last);
-      xa[i] = a.scale[static_cast<int64_t>(ra >> a.row_shift) * a.scale_row + blk * a.scale_block];
-      xb[i] = b.scale[static_cast<int64_t>(rb >> b.row_shift) * b.scale_row + blk * b.scale_block];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int x = tid + u * kMmThreads, r = x >> 3, c = x & 7;
-      *reinterpret_cast<u32x4*>(sa + r * 128 + ((c ^ r) & 7) * 16) = va[u];
-      *reinterpret_cast<u32x4*>(sb + r * 128 + ((c ^ r) & 7) * 16) = vb[u];
-    }
-    __syncthreads();
-    i32x8 fa[4], fb[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int ra = wi * 64 + i * 16 + l16, rb = wj * 64 + i * 16 + l16;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const i32x4 x = *reinterpret_cast<const i32x4*>(sa + ra * 128 + (((2 * kg + h) ^ ra) & 7) * 16);
-        const i32x4 y = *reinterpret_cast<const i32x4*>(sb + rb * 128 + (((2 * kg + h) ^ rb) & 7) * 16);
-#pragma unroll
-        for (int d = 0; d < 4; ++d) {
-          fa[i][4 * h + d] = x[d];
-          fb[i][4 * h + d] = y[d];
-        }
-      }
-    }
-    if (WIDE) {
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        bf16x8 wa[4], wb[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          wa[i] = widen(fa[i], g, scale_of(xa[i]));
-          wb[i] = widen(fb[i], g, scale_of(xb[i]));
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wa[i], wb[j], acc[i][j], 0, 0, 0);
-      }
-      continue;
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fa[i], fb[j], acc[i][j], 0, 0, 0, xa[i], 0, xb[j]);
-  }
-}
-
-// out[row][n]: A is the weights (a lane's four accumulators are consecutive
-// n), B the rows.
-__global__ __launch_bounds__(kMmThreads) void expert_gemm_kernel(
-    const int32_t* __restrict__ off, int32_t ne, const uint8_t* __restrict__ q, const uint8_t* __restrict__ q_scale,
-    int32_t K, const uint8_t* const* __restrict__ w, const uint8_t* const* __restrict__ w_scale, int32_t N,
-    uint16_t* __restrict__ out, int64_t cap, int64_t tiles, int32_t ntile) {
-  __shared__ __align__(16) uint8_t s_a[kMmTile * 128], s_b[kMmTile * 128];
-  const int32_t Kp = q_pitch(K), Ks = s_pitch(K);
-  const int lane = lane_id(), wv = threadIdx.x >> 6, wi = wv >> 1, wj = wv & 1;
-  for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
-    const int32_t tm = static_cast<int32_t>(t / ntile), tn = static_cast<int32_t>(t - static_cast<int64_t>(tm) * ntile);
-    const int32_t p = find_group(off, ne, cap, kMmTile, tm);
-    const int32_t o = group_row(off, p, cap), o1 = group_row(off, p + 1, cap);
-    const int64_t row0 = o + static_cast<int64_t>(tm - (o / kMmTile + p)) * kMmTile;
-    if (row0 >= o1) continue;
-    const uint8_t* wp = w[p];
-    const uint8_t* ws = w_scale[p];
-    if (wp == nullptr || ws == nullptr || (reinterpret_cast<uintptr_t>(wp) & 15) != 0 ||
-        (reinterpret_cast<uintptr_t>(ws) & 3) != 0)
-      continue;
-    const int32_t n0 = tn * kMmTile;
-    const int32_t rows = static_cast<int32_t>(min(static_cast<int64_t>(o1) - row0, static_cast<int64_t>(kMmTile)));
-    const int32_t cols = min(N - n0, kMmTile);
-    const Operand a{wp + static_cast<int64_t>(n0) * Kp, ws + static_cast<int64_t>(tn) * Ks, Kp, 128, Ks, 1, cols - 1, 7};
-    const Operand b{q + row0 * Kp, q_scale + row0 * Ks, Kp, 128, Ks, 1, rows - 1, 0};
-    f32x4 acc[4][4];
-    mm_tile<false>(a, b, Kp / 128, s_a, s_b, acc);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int r = wj * 64 + j * 16 + (lane & 15), c = wi * 64 + i * 16 + 4 * (lane >> 4);
-        if (r < rows && c < cols) {
-          u32x2 y;
-          y[0] = pack_bf16(acc[i][j][0], acc[i][j][1]);
-          y[1] = pack_bf16(acc[i][j][2], acc[i][j][3]);
-          *reinterpret_cast<u32x2*>(out + (row0 + r) * N + n0 + c) = y;
-        }
-      }
-  }
-}
 
 // Order of the tiles.  Workgroups go to the eight XCDs in turn; each XCD takes
 // one contiguous eighth of a walk that goes through eight row tiles by all
@@ -215,14 +69,18 @@ struct BigOperand {
 // A wave's 128 rows of A are read as 16-row fragments i = 0..7, fragment row m
 // being row 32 * (m / 4) + 4 * i + m % 4, so that a lane's accumulators
 // (fragment rows 4 * (l / 16) + r) are 32 consecutive rows: whole lines when
-// they are stored.  B's fragment j holds rows 16 * j + m.
+// they are stored.  B's halves are the tile's rows 0..127 and 128..255, of which
+// a wave has 64 each as fragments 0..3 and 4..7 (b_row).
 //
 // Half H of an operand's block is what the two waves along it read as
 // fragments 4H..4H+3, 64 rows each: row s of the half is this row of the tile.
 template <bool A, int H>
 __device__ __forceinline__ int half_row(int s) {
-  return A ? 128 * (s >> 6) + 32 * ((s >> 4) & 3) + 16 * H + (s & 15) : 128 * (s >> 6) + 64 * H + (s & 63);
+  return A ? 128 * (s >> 6) + 32 * ((s >> 4) & 3) + 16 * H + (s & 15) : 128 * H + s;
 }
+
+// Row m of B's fragment j of wave column wj.
+__device__ __forceinline__ int b_row(int wj, int j, int m) { return 128 * (j >> 2) + 64 * wj + 16 * (j & 3) + m; }
 
 // In LDS a row is eight 16-byte parts, part c at c ^ key(row).  64 banks are two
 // rows wide: an even and an odd row share a key, and the eight pairs of the
@@ -347,11 +205,11 @@ struct ScaleSource {
 };
 
 __device__ __forceinline__ void load_scales(const ScaleSource& s, int32_t block, ScaleWords& w) {
-  const int row0 = ((threadIdx.x >> 6) & 1) * 128 + (lane_id() & 15);
+  const int wj = (threadIdx.x >> 6) & 1, m = lane_id() & 15;
   w.a = *reinterpret_cast<const global_int*>(reinterpret_cast<uintptr_t>(s.a) + block);
 #pragma unroll
   for (int j = 0; j < 8; ++j)
-    w.b[j] = *reinterpret_cast<const int*>(s.b + static_cast<uint32_t>(min(row0 + 16 * j, s.last)) * s.pitch + block);
+    w.b[j] = *reinterpret_cast<const int*>(s.b + static_cast<uint32_t>(min(b_row(wj, j, m), s.last)) * s.pitch + block);
 }
 
 // Waits for the words here, and not at their first use in the loop.
@@ -395,6 +253,27 @@ __device__ __forceinline__ void big_step(const BigOperand& a, const BigOperand& 
   }
 }
 
+// The same for a tile whose rows are all in B's first half.
+template <int U>
+__device__ __forceinline__ void half_step(const BigOperand& a, const BigOperand& b, const Offsets& o, int32_t k,
+                                          int32_t blocks, uint8_t* alo, uint8_t* ahi, uint8_t* bx, uint8_t* next_alo,
+                                          uint8_t* next_bx, i32x8 (&fal)[4], i32x8 (&fah)[4], i32x8 (&fb)[4],
+                                          i32x8 (&fbn)[4], const ScaleSource& ss, ScaleWords& sw, ScaleWords& sn,
+                                          f32x4 (&acc)[8][8]) {
+  meet<12>();
+  quadrant<0, 0, U, kStrideA>(fal, fb, sw.a, sw.b, acc, ahi, o.read_a, fah, HalfLoad(a, k + 2, blocks, o.a[0], alo));
+  load_half(b, k + 2, blocks, o.b[0], bx);
+  meet<12>();
+  if (U == 2) load_scales(ss, min(k + 2, blocks - 1) & ~3, sn);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) fbn[i] = read_fragment<kStrideB>(next_bx, o.read_b, i);
+  quadrant<4, 0, U, kStrideA>(fah, fb, sw.a, sw.b, acc, next_alo, o.read_a, fal, HalfLoad(a, k + 2, blocks, o.a[1], ahi));
+  if (U == 3) {
+    sw = sn;
+    products_done();
+  }
+}
+
 // What the products of one segment share.
 struct GemmArgs {
   const int32_t* off;
@@ -416,18 +295,31 @@ __device__ __forceinline__ bool usable(const uint8_t* w, const uint8_t* ws) {
 }
 
 // out[row][n]: A is the weights (a lane holds 32 consecutive n of a row), B the
-// rows; one 256 x 256 tile a workgroup, four waves of 128 x 128.
-__global__ __launch_bounds__(kMmThreads, 1) void expert_gemm_big_kernel(GemmArgs g, int32_t ntile) {
+// rows; one tile of 256 columns and up to `unit` rows a workgroup, four waves of
+// 128 x 128 (128 x 64 when the rows fit B's first half).
+//
+// Bound by the matrix units' rate at the clock they leave (about 2.0 GHz), and
+// next to that by the loads into LDS: alone, the products of a block of a full
+// tile take 1.0-1.3 us, its 64 KiB of loads 1.5 us, together 1.55 us.  Larger
+// tiles do not fit the registers.  32768 rows by 6 experts of 4096 x 7168: 781 us,
+// 2.46 PFLOP/s; 8192 x 8192 x 8192: 430 us, 2.56 PFLOP/s (a library's plain 8-bit
+// product reaches 2.71-2.78 there).  Measured and not kept: one workgroup a CU that
+// walks the tiles and loads the next one's blocks before it stores (829 us: the
+// hardware's dealing balances better); a barrier a quadrant (853 us against 875,
+// before the loads were spread); all of a half's loads at once (875 us against
+// 807); non-temporal stores (1009 us against 881).
+__global__ __launch_bounds__(kMmThreads, 1) void expert_gemm_big_kernel(GemmArgs g, int32_t ntile,
+                                                                        int32_t unit) {
   __shared__ __align__(16) uint8_t a00[kHalfBytes], a01[kHalfBytes], a10[kHalfBytes], a11[kHalfBytes];
   __shared__ __align__(16) uint8_t b00[kHalfBytes], b01[kHalfBytes], b10[kHalfBytes], b11[kHalfBytes];
   const int32_t Kp = q_pitch(g.K), Ks = s_pitch(g.K), blocks = Kp / 128;
   const int lane = lane_id(), l16 = lane & 15, kg = lane >> 4;
   const int wv = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6)), wi = wv >> 1, wj = wv & 1;
-  const int32_t mtile = row_tiles(g.off, g.ne, g.cap, kBigTile);
+  const int32_t mtile = row_tiles(g.off, g.ne, g.cap, unit);
   const int64_t tiles = static_cast<int64_t>(mtile) * ntile;
   if (blockIdx.x >= tiles) return;
   const Tile2 at = tile_order(blockIdx.x, tiles, mtile, ntile);
-  const RowTile rt = find_row_tile(g.off, g.ne, g.cap, kBigTile, at.m);
+  const RowTile rt = find_row_tile(g.off, g.ne, g.cap, unit, at.m);
   const uint8_t* wp = g.w[rt.p];
   const uint8_t* ws = g.w_scale[rt.p];
   if (!usable(wp, ws)) return;
@@ -450,47 +342,155 @@ __global__ __launch_bounds__(kMmThreads, 1) void expert_gemm_big_kernel(GemmArgs
   ScaleWords sw, sn;
   load_scales(ss, 0, sw);
   settle(sw);
-  load_half(a, 0, blocks, o.a[0], a00);
-  load_half(b, 0, blocks, o.b[0], b00);
-  load_half(b, 0, blocks, o.b[1], b01);
-  load_half(a, 0, blocks, o.a[1], a01);
-  load_half(a, 1, blocks, o.a[0], a10);
-  load_half(b, 1, blocks, o.b[1], b11);
-  load_half(b, 1, blocks, o.b[0], b10);
-  load_half(a, 1, blocks, o.a[1], a11);
   f32x4 acc[8][8];
 #pragma unroll
   for (int i = 0; i < 8; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   i32x8 fal[4], fah[4], fb0[4], fb1[4];
-  meet<24>();
+  const auto store = [&](int j0, int j1) {
+    const int c = wi * 128 + 32 * kg;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    fal[i] = read_fragment<kStrideA>(a00, o.read_a, i);
-    fb0[i] = read_fragment<kStrideB>(b00, o.read_b, i);
-  }
-  for (int32_t k = 0; k < blocks; k += 4) {
-    big_step<0>(a, b, o, k, blocks, a00, a01, b00, b01, a10, b11, fal, fah, fb0, fb1, ss, sw, sn, acc);
-    big_step<1>(a, b, o, k + 1, blocks, a10, a11, b11, b10, a00, b00, fal, fah, fb1, fb0, ss, sw, sn, acc);
-    big_step<2>(a, b, o, k + 2, blocks, a00, a01, b00, b01, a10, b11, fal, fah, fb0, fb1, ss, sw, sn, acc);
-    big_step<3>(a, b, o, k + 3, blocks, a10, a11, b11, b10, a00, b00, fal, fah, fb1, fb0, ss, sw, sn, acc);
-  }
-  const int c = wi * 128 + 32 * kg;
+    for (int j = j0; j < j1; ++j) {
+      const int r = b_row(wj, j, l16);
+      if (r < rows) {
+        u32x4* d = reinterpret_cast<u32x4*>(g.out + (rt.row0 + r) * g.N + n0 + c);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int r = wj * 128 + 16 * j + l16;
-    if (r < rows) {
-      u32x4* d = reinterpret_cast<u32x4*>(g.out + (rt.row0 + r) * g.N + n0 + c);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (c + 8 * i < cols)
-          d[i] = u32x4{pack_bf16(acc[2 * i][j][0], acc[2 * i][j][1]), pack_bf16(acc[2 * i][j][2], acc[2 * i][j][3]),
-                       pack_bf16(acc[2 * i + 1][j][0], acc[2 * i + 1][j][1]),
-                       pack_bf16(acc[2 * i + 1][j][2], acc[2 * i + 1][j][3])};
+        for (int i = 0; i < 4; ++i)
+          if (c + 8 * i < cols)
+            d[i] = u32x4{pack_bf16(acc[2 * i][j][0], acc[2 * i][j][1]), pack_bf16(acc[2 * i][j][2], acc[2 * i][j][3]),
+                         pack_bf16(acc[2 * i + 1][j][0], acc[2 * i + 1][j][1]),
+                         pack_bf16(acc[2 * i + 1][j][2], acc[2 * i + 1][j][3])};
+      }
     }
+  };
+  load_half(a, 0, blocks, o.a[0], a00);
+  load_half(b, 0, blocks, o.b[0], b00);
+  if (rows > 128) {
+    load_half(b, 0, blocks, o.b[1], b01);
+    load_half(a, 0, blocks, o.a[1], a01);
+    load_half(a, 1, blocks, o.a[0], a10);
+    load_half(b, 1, blocks, o.b[1], b11);
+    load_half(b, 1, blocks, o.b[0], b10);
+    load_half(a, 1, blocks, o.a[1], a11);
+    meet<24>();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      fal[i] = read_fragment<kStrideA>(a00, o.read_a, i);
+      fb0[i] = read_fragment<kStrideB>(b00, o.read_b, i);
+    }
+    for (int32_t k = 0; k < blocks; k += 4) {
+      big_step<0>(a, b, o, k, blocks, a00, a01, b00, b01, a10, b11, fal, fah, fb0, fb1, ss, sw, sn, acc);
+      big_step<1>(a, b, o, k + 1, blocks, a10, a11, b11, b10, a00, b00, fal, fah, fb1, fb0, ss, sw, sn, acc);
+      big_step<2>(a, b, o, k + 2, blocks, a00, a01, b00, b01, a10, b11, fal, fah, fb0, fb1, ss, sw, sn, acc);
+      big_step<3>(a, b, o, k + 3, blocks, a10, a11, b11, b10, a00, b00, fal, fah, fb1, fb0, ss, sw, sn, acc);
+    }
+    store(0, 8);
+  } else {
+    load_half(a, 0, blocks, o.a[1], a01);
+    load_half(a, 1, blocks, o.a[0], a10);
+    load_half(b, 1, blocks, o.b[0], b10);
+    load_half(a, 1, blocks, o.a[1], a11);
+    meet<16>();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      fal[i] = read_fragment<kStrideA>(a00, o.read_a, i);
+      fb0[i] = read_fragment<kStrideB>(b00, o.read_b, i);
+    }
+    for (int32_t k = 0; k < blocks; k += 4) {
+      half_step<0>(a, b, o, k, blocks, a00, a01, b00, a10, b10, fal, fah, fb0, fb1, ss, sw, sn, acc);
+      half_step<1>(a, b, o, k + 1, blocks, a10, a11, b10, a00, b00, fal, fah, fb1, fb0, ss, sw, sn, acc);
+      half_step<2>(a, b, o, k + 2, blocks, a00, a01, b00, a10, b10, fal, fah, fb0, fb1, ss, sw, sn, acc);
+      half_step<3>(a, b, o, k + 3, blocks, a10, a11, b10, a00, b00, fal, fah, fb1, fb0, ss, sw, sn, acc);
+    }
+    store(0, 4);
   }
   meet<0>();  // no load outlives the workgroup's LDS
+}
+
+// ------------------------------------------------------------------------
+// Few rows an expert: the weights are the traffic
+// ------------------------------------------------------------------------
+constexpr int kThinWaves = 4;
+constexpr int kThinThreads = 64 * kThinWaves;
+constexpr int kThinRows = 16, kThinCols = 64;
+
+// Fragment of 16 rows: lane's two 16-byte parts kg and kg + 4 of its row, so
+// that one load covers 64 bytes of each row in order.  Both operands take the
+// same parts, so the products pair the same k.
+__device__ __forceinline__ i32x8 thin_fragment(const uint8_t* row) {
+  return __builtin_shufflevector(*reinterpret_cast<const i32x4*>(row), *reinterpret_cast<const i32x4*>(row + 64), 0, 1, 2, 3,
+                                 4, 5, 6, 7);
+}
+
+// FN * 16 weight rows by NJ * 16 rows.  The four waves split the blocks of 128
+// (wave v takes v, v + 4, ...), every weight byte goes from memory to the
+// registers of the one wave that uses it, DEPTH blocks ahead, and the waves'
+// sums meet in LDS and are added in wave order.  Bound by HBM: 41 rows by 6
+// experts of 4096 x 7168 (177 MB) take 31 us, 5.7 TB/s.  Eight or sixteen waves a
+// tile take 34 and 38 us, loads two blocks ahead 40 (fewer waves fit), 128
+// columns a tile 39, 32 rows 37; non-temporal loads 46.
+__global__ __launch_bounds__(kThinThreads) void expert_gemm_thin_kernel(GemmArgs g, int32_t ntile) {
+  constexpr int FN = kThinCols / 16;
+  __shared__ __align__(16) float s_sum[kThinWaves][kThinRows][kThinCols + 4];
+  const int32_t Kp = q_pitch(g.K), Ks = s_pitch(g.K), blocks = Kp / 128;
+  const int lane = lane_id(), l16 = lane & 15, kg = lane >> 4;
+  const int wv = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
+  const int32_t mtile = row_tiles(g.off, g.ne, g.cap, kThinRows);
+  const int64_t tiles = static_cast<int64_t>(mtile) * ntile;
+  for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+    const int64_t full = tiles & ~int64_t{7};
+    const int64_t at = t < full ? (t & 7) * (full >> 3) + (t >> 3) : t;  // an XCD's tiles follow each other
+    const int32_t tn = static_cast<int32_t>(at / mtile), tm = static_cast<int32_t>(at - static_cast<int64_t>(tn) * mtile);
+    const RowTile rt = find_row_tile(g.off, g.ne, g.cap, kThinRows, tm);
+    const uint8_t* wp = g.w[rt.p];
+    const uint8_t* ws = g.w_scale[rt.p];
+    if (!usable(wp, ws)) continue;
+    const int32_t n0 = tn * kThinCols, cols = min(g.N - n0, kThinCols);
+    const uint8_t* pa[FN];
+#pragma unroll
+    for (int i = 0; i < FN; ++i) pa[i] = wp + static_cast<int64_t>(n0 + min(16 * i + l16, cols - 1)) * Kp + kg * 16;
+    const int64_t r = rt.row0 + min(l16, rt.rows - 1);
+    const uint8_t* pb = g.q + r * Kp + kg * 16;
+    const uint8_t* sa = ws + static_cast<int64_t>(n0 / 128) * Ks;
+    const uint8_t* sb = g.q_scale + r * Ks;
+    f32x4 acc[FN];
+#pragma unroll
+    for (int i = 0; i < FN; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    i32x8 fa[FN], fb;
+    int xa, xb;
+    const auto load = [&](int32_t block) {
+      const int32_t b = min(block, blocks - 1);
+#pragma unroll
+      for (int i = 0; i < FN; ++i) fa[i] = thin_fragment(pa[i] + b * 128);
+      fb = thin_fragment(pb + b * 128);
+      xa = sa[b];
+      xb = sb[b];
+    };
+    load(wv);
+    for (int32_t b = wv; b < blocks; b += kThinWaves) {
+#pragma unroll
+      for (int i = 0; i < FN; ++i)
+        acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fa[i], fb, acc[i], 0, 0, 0, xa, 0, xb);
+      load(b + kThinWaves);
+    }
+    __syncthreads();  // the previous tile's sums have been read
+#pragma unroll
+    for (int i = 0; i < FN; ++i) *reinterpret_cast<f32x4*>(&s_sum[wv][l16][16 * i + 4 * kg]) = acc[i];
+    __syncthreads();
+    // two columns a thread
+    for (int u = threadIdx.x; u < kThinRows * kThinCols / 2; u += kThinThreads) {
+      const int row = u / (kThinCols / 2), c = 2 * (u % (kThinCols / 2));
+      if (row >= rt.rows || c >= cols) continue;
+      float lo = 0.f, hi = 0.f;
+#pragma unroll
+      for (int v = 0; v < kThinWaves; ++v) {
+        lo += s_sum[v][row][c];
+        hi += s_sum[v][row][c + 1];
+      }
+      *reinterpret_cast<uint32_t*>(g.out + (rt.row0 + row) * g.N + n0 + c) = pack_bf16(lo, hi);
+    }
+  }
 }
 
 // ------------------------------------------------------------------------
@@ -530,7 +530,8 @@ struct WideTile {
   BigOperand a, b;
   const uint8_t *scale_a, *scale_b;  // scale bytes of the tile's rows, block 0
   int32_t pitch_a, pitch_b;          // scale bytes a block
-  int32_t row_a, row_b;              // this lane's row of fragment 0
+  int32_t row_a;                     // this lane's row of A's fragment 0
+  int32_t wj, l16;
   uint32_t off_a[2][4], off_b[2][4];
   int at_a[4], at_b[4];              // LDS offset of this lane's eight bytes g, in a half
 };
@@ -587,7 +588,7 @@ __device__ __forceinline__ void wide_block(const WideTile& t, WideState& w, int3
       if (j == 6 || j == 7) {
         if (n >= 2 && n < 10) {
           if (j == 6) w.na[n - 2] = scale_byte(sa, t.row_a + 4 * (n - 2), t.a.last);
-          if (j == 7) w.nb[n - 2] = scale_byte(sb, t.row_b + 16 * (n - 2), t.b.last);
+          if (j == 7) w.nb[n - 2] = scale_byte(sb, b_row(t.wj, n - 2, t.l16), t.b.last);
         }
         if (n >= 20 && n < 24) (j == 6 ? load_bl : load_bh).issue(n - 20);
         if (n >= 27 && n < 31) (j == 6 ? load_al : load_ah).issue(n - 27);
@@ -611,6 +612,13 @@ __device__ __forceinline__ int32_t expert_of_rank(const int32_t* off, int32_t ne
 }
 
 // grads[p][n][k]: A is x (a lane holds 32 consecutive k of a row n), B is dy.
+//
+// Bound by the bf16 products at the clock they leave.  32768 rows, 6 experts of
+// 4096 x 7168: 1352 us, 1.42 PFLOP/s (a library's plain bf16 product reaches 1.24
+// at 8192 x 8192 x 8192); without the loads 1200 us.  With the tiles dealt to the
+// XCDs in one walk over all experts it took 2260 us: an XCD got whole experts.
+// Widening spread over all eight products of a step instead of the first four:
+// 1404 us.
 __global__ __launch_bounds__(kMmThreads, 1) void expert_wgrad_big_kernel(
     const int32_t* off, int32_t ne, const uint8_t* dyt, const uint8_t* dyt_scale, int32_t N, const uint8_t* xt,
     const uint8_t* xt_scale, int32_t K, int64_t cap, float* const* grads, bool accumulate, int32_t ntile,
@@ -645,7 +653,8 @@ __global__ __launch_bounds__(kMmThreads, 1) void expert_wgrad_big_kernel(
     t.pitch_a = K;
     t.pitch_b = N;
     t.row_a = wi * 128 + 32 * (l16 >> 2) + (l16 & 3);
-    t.row_b = wj * 128 + l16;
+    t.wj = wj;
+    t.l16 = l16;
     load_offsets<true, 0>(t.a, t.off_a[0]);
     load_offsets<true, 1>(t.a, t.off_a[1]);
     load_offsets<false, 0>(t.b, t.off_b[0]);
@@ -662,7 +671,7 @@ __global__ __launch_bounds__(kMmThreads, 1) void expert_wgrad_big_kernel(
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       w.sa[j] = scale_of(scale_byte(t.scale_a, t.row_a + 4 * j, t.a.last));
-      w.sb[j] = scale_of(scale_byte(t.scale_b, t.row_b + 16 * j, t.b.last));
+      w.sb[j] = scale_of(scale_byte(t.scale_b, b_row(wj, j, l16), t.b.last));
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) asm volatile("" : "+v"(w.sa[j]), "+v"(w.sb[j]));
@@ -700,7 +709,7 @@ __global__ __launch_bounds__(kMmThreads, 1) void expert_wgrad_big_kernel(
   const int c = wi * 128 + 32 * kg;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const int r = wj * 128 + 16 * j + l16;
+    const int r = b_row(wj, j, l16);
     if (r >= rows) continue;
     float* d = out + static_cast<int64_t>(n0 + r) * K + k0 + c;
 #pragma unroll
@@ -719,50 +728,6 @@ __global__ __launch_bounds__(kMmThreads, 1) void expert_wgrad_big_kernel(
   meet<0>();  // no load outlives the workgroup's LDS
 }
 
-// grads[p][n][k]: A is x (four consecutive k a lane), B is dy.
-__global__ __launch_bounds__(kMmThreads) void expert_wgrad_kernel(
-    const int32_t* __restrict__ off, int32_t ne, const uint8_t* __restrict__ dyt, const uint8_t* __restrict__ dyt_scale,
-    int32_t N, const uint8_t* __restrict__ xt, const uint8_t* __restrict__ xt_scale, int32_t K, int64_t cap,
-    float* const* __restrict__ grads, bool accumulate, int64_t tiles, int32_t ntile, int32_t ktile) {
-  __shared__ __align__(16) uint8_t s_a[kMmTile * 128], s_b[kMmTile * 128];
-  const int lane = lane_id(), wv = threadIdx.x >> 6, wi = wv >> 1, wj = wv & 1;
-  for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
-    const int32_t per = ntile * ktile;
-    const int32_t p = static_cast<int32_t>(t / per), rest = static_cast<int32_t>(t - static_cast<int64_t>(p) * per);
-    const int32_t tn = rest / ktile, tk = rest - tn * ktile;
-    float* g = grads[p];
-    if (g == nullptr) continue;
-    const int32_t o = group_row(off, p, cap), o1 = group_row(off, p + 1, cap);
-    const int32_t blocks = max(ceil_div(o1 - o, kQBlock), 0);
-    if (blocks == 0 && accumulate) continue;
-    const int64_t b0 = o / kQBlock + p;
-    const int32_t n0 = tn * kMmTile, k0 = tk * kMmTile;
-    const int32_t rows = min(N - n0, kMmTile), cols = min(K - k0, kMmTile);
-    const Operand a{xt + (b0 * K + k0) * kQBlock, xt_scale + b0 * K + k0, 128, static_cast<int64_t>(K) * kQBlock, 1, K, cols - 1, 0};
-    const Operand b{dyt + (b0 * N + n0) * kQBlock, dyt_scale + b0 * N + n0, 128, static_cast<int64_t>(N) * kQBlock, 1, N, rows - 1, 0};
-    f32x4 acc[4][4];
-    mm_tile<true>(a, b, blocks, s_a, s_b, acc);
-    const bool vec = (reinterpret_cast<uintptr_t>(g) & 15) == 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int r = wj * 64 + j * 16 + (lane & 15), c = wi * 64 + i * 16 + 4 * (lane >> 4);
-        if (r < rows && c < cols) {
-          float* d = g + static_cast<int64_t>(n0 + r) * K + k0 + c;
-          f32x4 y = acc[i][j];
-          if (vec) {
-            if (accumulate) y += *reinterpret_cast<const f32x4*>(d);
-            *reinterpret_cast<f32x4*>(d) = y;
-          } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) d[e] = accumulate ? d[e] + y[e] : y[e];
-          }
-        }
-      }
-  }
-}
-
 uint32_t mm_grid(int64_t tiles) { return static_cast<uint32_t>(tiles < (1 << 20) ? tiles : (1 << 20)); }
 
 }  // namespace
@@ -771,17 +736,27 @@ hipError_t launch_expert_gemm(const int32_t* off, int32_t ne, const uint8_t* q, 
                               const uint8_t* const* w, const uint8_t* const* w_scale, int32_t N, uint16_t* out,
                               int64_t cap, hipStream_t st) {
   if (ne == 0 || cap == 0) return hipSuccess;
-  if (cap / ne >= 64) {
-    const int32_t ntile = ceil_div(N, kBigTile), mtile = static_cast<int32_t>(cap / kBigTile) + ne;
-    const GemmArgs g{off, ne, q, q_scale, K, w, w_scale, N, out, cap};
-    hipLaunchKernelGGL(expert_gemm_big_kernel, dim3(static_cast<uint32_t>(static_cast<int64_t>(mtile) * ntile)),
-                       dim3(kMmThreads), 0, st, g, ntile);
+  const GemmArgs g{off, ne, q, q_scale, K, w, w_scale, N, out, cap};
+  const int32_t nbig = ceil_div(N, kBigTile);
+  // Few rows.  With 6 experts of 4096 x 7168 (96 big tiles, too few to draw all
+  // of the memory's rate) thin tiles take 21 / 30 / 32 / 40 / 58 us at 1 / 4 / 8 /
+  // 12 / 16 rows an expert, big ones 46 / 46 / 49 / 50 / 54; with 24 experts of
+  // 2048 x 5120 (192 big tiles) 50 / 57 us at 4 / 8 rows, big ones 49 / 50.
+  if (cap <= 4 * static_cast<int64_t>(ne) || (cap <= 12 * static_cast<int64_t>(ne) && static_cast<int64_t>(ne) * nbig < 128)) {
+    const int32_t ntile = ceil_div(N, kThinCols);
+    const int64_t tiles = (cap / kThinRows + ne) * ntile;
+    hipLaunchKernelGGL(expert_gemm_thin_kernel, dim3(mm_grid(tiles)), dim3(kThinThreads), 0, st, g, ntile);
     return hipGetLastError();
   }
-  const int32_t ntile = ceil_div(N, kMmTile);
-  const int64_t tiles = (cap / kMmTile + ne) * ntile;
-  hipLaunchKernelGGL(expert_gemm_kernel, dim3(mm_grid(tiles)), dim3(kMmThreads), 0, st, off, ne, q, q_scale, K, w,
-                     w_scale, N, out, cap, tiles, ntile);
+  // Rows a tile, 256 or 128: a tile of 128 takes about 11/15 of the time of one of
+  // 256 (49 and 66 us a round at K = 5120), so what counts is the rounds of 256
+  // workgroups; an expert's last tile is half full on average.  64 rows for each of
+  // 24 experts: 59 us in tiles of 128, 66 in tiles of 256; 200: 99 and 117; 500
+  // for each of 6 experts of 4096 x 7168: 122 and 91; 5461: 1010 and 799.
+  const auto rounds = [&](int32_t u) { return ((cap / u + ne / 2 + 1) * nbig + 255) / 256; };
+  const int32_t unit = 11 * rounds(128) < 15 * rounds(256) ? 128 : 256;
+  const int64_t tiles = (cap / unit + ne) * nbig;
+  hipLaunchKernelGGL(expert_gemm_big_kernel, dim3(static_cast<uint32_t>(tiles)), dim3(kMmThreads), 0, st, g, nbig, unit);
   return hipGetLastError();
 }
 
@@ -789,16 +764,9 @@ hipError_t launch_expert_wgrad(const int32_t* off, int32_t ne, const uint8_t* dy
                                const uint8_t* xt, const uint8_t* xt_scale, int32_t K, int64_t cap, float* const* grads,
                                bool accumulate, hipStream_t st) {
   if (ne == 0) return hipSuccess;
-  if (true) {
-    const int32_t ntile = ceil_div(N, kBigTile), ktile = ceil_div(K, kBigTile);
-    hipLaunchKernelGGL(expert_wgrad_big_kernel, dim3(static_cast<uint32_t>(ne * ntile * ktile)), dim3(kMmThreads), 0, st,
-                       off, ne, dyt, dyt_scale, N, xt, xt_scale, K, cap, grads, accumulate, ntile, ktile);
-    return hipGetLastError();
-  }
-  const int32_t ntile = ceil_div(N, kMmTile), ktile = ceil_div(K, kMmTile);
-  const int64_t tiles = static_cast<int64_t>(ne) * ntile * ktile;
-  hipLaunchKernelGGL(expert_wgrad_kernel, dim3(mm_grid(tiles)), dim3(kMmThreads), 0, st, off, ne, dyt, dyt_scale, N, xt,
-                     xt_scale, K, cap, grads, accumulate, tiles, ntile, ktile);
+  const int32_t ntile = ceil_div(N, kBigTile), ktile = ceil_div(K, kBigTile);
+  hipLaunchKernelGGL(expert_wgrad_big_kernel, dim3(static_cast<uint32_t>(ne * ntile * ktile)), dim3(kMmThreads), 0, st, off,
+                     ne, dyt, dyt_scale, N, xt, xt_scale, K, cap, grads, accumulate, ntile, ktile);
   return hipGetLastError();
 }
 

@@ -253,6 +253,17 @@ def test_expert_gemm_real_values(N, K, loads):
     assert (np.abs(got - want) <= slack + BF16_STEP * (np.abs(want) + slack)).all()
 
 
+@pytest.mark.parametrize("loads,N,K", [([700, 0, 300, 211], 8200, 392), ([130, 257, 1000], 6152, 1160)])
+def test_expert_gemm_tiles_of_256_rows(loads, N, K):
+    """Enough tiles for the full height; ragged rows, columns and blocks, and blocks left over from four."""
+    say(f"expert_gemm 256-row tiles loads={loads} N={N} K={K}")
+    rng = np.random.default_rng([N, K])
+    seg, q, qs, w, ws = operands(rng, loads, N, K, whole=True)
+    got = run_gemm(seg, q, qs, w, ws, N, K)[:seg.rows]
+    want, _ = to_bf16(X.expert_gemm(*gemm_values(seg, q, qs, w, ws), seg.off) + 0.0)
+    assert np.array_equal(np.where(got == 0x8000, 0, got), np.where(want == 0x8000, 0, want))
+
+
 def test_expert_gemm_skips_missing_weights_and_cuts_at_the_capacity():
     rng = np.random.default_rng(8)
     seg, q, qs, w, ws = operands(rng, [40, 300, 5, 60], 264, 136, whole=True)
@@ -293,7 +304,8 @@ def columns(rng, seg, width, whole):
 @pytest.mark.parametrize("accumulate", [False, True])
 @pytest.mark.parametrize("shift", [0, 1])
 @pytest.mark.parametrize("loads,N,K", [([1], 8, 8), ([127, 1, 0, 129, 257], 136, 72), ([300, 0, 40], 264, 520),
-                                       ([1] * 40 + [0] * 30 + [130], 72, 136), ([640], 384, 256)])
+                                       ([1] * 40 + [0] * 30 + [130], 72, 136), ([640], 384, 256),
+                                       ([129, 385, 0, 513], 776, 520)])
 def test_expert_wgrad_whole_numbers(loads, N, K, shift, accumulate):
     say(f"expert_wgrad loads={loads[:8]} N={N} K={K} shift={shift} accumulate={accumulate}")
     rng = np.random.default_rng([N, K, sum(loads)])
