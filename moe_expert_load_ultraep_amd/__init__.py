@@ -124,7 +124,8 @@ def _stream(stream) -> Optional[int]:
     if stream is not None:
         return int(stream) if isinstance(stream, int) else stream.cuda_stream
     import torch
-    return torch.cuda.current_stream().cuda_stream
+    # the current stream's handle without building a Stream object (2.7 us of a 5 us call)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _ptr(t) -> Optional[int]:
@@ -299,21 +300,36 @@ def pointer_table(tensors, device="cuda"):
     return torch.tensor([0 if t is None else t.data_ptr() for t in tensors], dtype=torch.int64).to(device)
 
 
-def _is(t, dtypes, shape) -> bool:
-    """A contiguous tensor of the current device with one of the types and this shape (None: any extent)."""
-    import torch
-    return (t.is_cuda and t.device.index == torch.cuda.current_device() and t.dtype in dtypes and t.is_contiguous()
-            and len(t.shape) == len(shape) and all(w is None or n == w for n, w in zip(t.shape, shape)))
-
-
-def _need(fn: str, *ok) -> None:
-    if not all(ok):
-        raise UltraEPError(fn, -1)
+_TYPES = None
 
 
 def _types():
+    """(current device, e4m3 types, bf16 types, int64, int32): what a call checks its buffers against."""
+    global _TYPES
     import torch
-    return ({torch.uint8, torch.float8_e4m3fn}, {torch.bfloat16, torch.int16, torch.uint16}, {torch.int64}, {torch.int32})
+    if _TYPES is None:
+        _TYPES = (frozenset({torch.uint8, torch.float8_e4m3fn}),
+                  frozenset({torch.bfloat16, torch.int16, torch.uint16}), frozenset({torch.int64}),
+                  frozenset({torch.int32}))
+    return (torch.cuda.current_device() if torch.cuda.is_initialized() else None, *_TYPES)
+
+
+def _is(t, dev, dtypes, *shape) -> bool:
+    """A contiguous tensor of the current device with one of the types and this shape; the first extent may be
+    None (any)."""
+    s = t.shape
+    return (t.get_device() == dev and t.dtype in dtypes and len(s) == len(shape)
+            and (s == shape if shape[0] is not None else s[1:] == shape[1:]) and t.is_contiguous())
+
+
+def _is_plan(ctx, plan, dev) -> bool:
+    """One plan record of the context."""
+    return plan.get_device() == dev and plan.is_contiguous() and plan.numel() * plan.element_size() >= ctx.plan_bytes
+
+
+def _need(fn: str, ok: bool) -> None:
+    if not ok:
+        raise UltraEPError(fn, -1)
 
 
 def ultraep_permute_quant(ctx: Context, plan, inv, k: int, hidden, p_begin: int, p_end: int, q=None, q_scale=None,
@@ -324,20 +340,20 @@ def ultraep_permute_quant(ctx: Context, plan, inv, k: int, hidden, p_begin: int,
     qt [blocks, H, 128] with qt_scale [blocks, H] the columns form.  `rows` is the segment's capacity,
     by default q's rows (with qt alone it has to be given)."""
     fn = "ultraep_permute_quant"
-    f8, f16, _, i32 = _types()
-    _need(fn, (q is None) == (q_scale is None), (qt is None) == (qt_scale is None), q is not None or qt is not None,
-          _is(hidden, f16, (None, None)), inv is None or (inv.is_cuda and inv.dtype in i32 and inv.is_contiguous()))
+    dev, f8, f16, _, i32 = _types()
+    _need(fn, (q is None) == (q_scale is None) and (qt is None) == (qt_scale is None) and not (q is None and qt is None)
+          and hidden.dim() == 2 and (rows is not None or q is not None))
     H = hidden.shape[1]
     if rows is None:
-        _need(fn, q is not None)
         rows = q.shape[0]
-    if q is not None:
-        _need(fn, _is(q, f8, (None, quant_pitch(H))), _is(q_scale, f8, (q.shape[0], quant_scale_pitch(H))),
-              rows <= q.shape[0])
     blocks = 0
+    _need(fn, _is_plan(ctx, plan, dev) and _is(hidden, dev, f16, None, H) and (inv is None or _is(inv, dev, i32, None)))
+    if q is not None:
+        _need(fn, _is(q, dev, f8, None, quant_pitch(H)) and _is(q_scale, dev, f8, q.shape[0], quant_scale_pitch(H))
+              and rows <= q.shape[0])
     if qt is not None:
         blocks = qt.shape[0]
-        _need(fn, _is(qt, f8, (None, H, QUANT_BLOCK)), _is(qt_scale, f8, (blocks, H)))
+        _need(fn, _is(qt, dev, f8, None, H, QUANT_BLOCK) and _is(qt_scale, dev, f8, blocks, H))
     st = lib().ultraep_permute_quant(ctx.handle, _ptr(plan), _ptr(inv), k, _ptr(hidden), hidden.shape[0], H, p_begin,
                                      p_end, _ptr(q), _ptr(q_scale), _ptr(qt), _ptr(qt_scale), rows, blocks,
                                      _stream(stream))
@@ -349,14 +365,14 @@ def ultraep_weight_quant(ctx: Context, weights, n: int, N: int, K: int, q=None, 
     """weights: int64 device tensor [n] of pointers to bf16 [N, K]; q [n, N, quant_pitch(K)] with q_scale
     [n, ceil(N/128), quant_scale_pitch(K)], and the transposes' qt [n, K, quant_pitch(N)] with qt_scale."""
     fn = "ultraep_weight_quant"
-    f8, _, i64, _ = _types()
-    _need(fn, (q is None) == (q_scale is None), (qt is None) == (qt_scale is None), _is(weights, i64, (None,)),
-          weights.shape[0] >= n)
+    dev, f8, _, i64, _ = _types()
+    _need(fn, (q is None) == (q_scale is None) and (qt is None) == (qt_scale is None)
+          and _is(weights, dev, i64, None) and weights.shape[0] >= n)
     for a, b, x, xs in ((N, K, q, q_scale), (K, N, qt, qt_scale)):
         if x is not None:
-            _need(fn, _is(x, f8, (None, a, quant_pitch(b))),
-                  _is(xs, f8, (None, quant_pitch(a) // QUANT_BLOCK, quant_scale_pitch(b))),
-                  x.shape[0] >= n, xs.shape[0] >= n)
+            _need(fn, _is(x, dev, f8, None, a, quant_pitch(b))
+                  and _is(xs, dev, f8, None, quant_pitch(a) // QUANT_BLOCK, quant_scale_pitch(b))
+                  and x.shape[0] >= n and xs.shape[0] >= n)
     st = lib().ultraep_weight_quant(ctx.handle, _ptr(weights), n, N, K, _ptr(q), _ptr(q_scale), _ptr(qt),
                                     _ptr(qt_scale), _stream(stream))
     _check(fn, st)
@@ -368,10 +384,10 @@ def ultraep_expert_gemm(ctx: Context, plan, q, q_scale, K: int, w, w_scale, N: i
 
     w, w_scale: int64 device tensors [p_end - p_begin] of pointers to the quantised weights and scales."""
     fn = "ultraep_expert_gemm"
-    f8, f16, i64, _ = _types()
-    _need(fn, _is(q, f8, (None, quant_pitch(K))), _is(q_scale, f8, (q.shape[0], quant_scale_pitch(K))),
-          _is(w, i64, (None,)), _is(w_scale, i64, (None,)), w.shape[0] >= p_end - p_begin,
-          w_scale.shape[0] >= p_end - p_begin, _is(out, f16, (None, N)))
+    dev, f8, f16, i64, _ = _types()
+    _need(fn, _is_plan(ctx, plan, dev) and _is(q, dev, f8, None, quant_pitch(K)) and _is(q_scale, dev, f8, q.shape[0], quant_scale_pitch(K))
+          and _is(w, dev, i64, None) and _is(w_scale, dev, i64, None) and w.shape[0] >= p_end - p_begin
+          and w_scale.shape[0] >= p_end - p_begin and _is(out, dev, f16, None, N))
     st = lib().ultraep_expert_gemm(ctx.handle, _ptr(plan), _ptr(q), _ptr(q_scale), K, _ptr(w), _ptr(w_scale), N,
                                    p_begin, p_end, _ptr(out), min(out.shape[0], q.shape[0]), _stream(stream))
     _check(fn, st)
@@ -381,34 +397,35 @@ def ultraep_expert_wgrad(ctx: Context, plan, dyt, dyt_scale, N: int, xt, xt_scal
                          rows: int, grads, accumulate: bool = False, stream=None) -> None:
     """grads: int64 device tensor [p_end - p_begin] of pointers to fp32 [N, K]; rows: the segment's capacity."""
     fn = "ultraep_expert_wgrad"
-    f8, _, i64, _ = _types()
-    _need(fn, rows >= 0, _is(dyt, f8, (None, N, QUANT_BLOCK)), _is(dyt_scale, f8, (dyt.shape[0], N)),
-          _is(xt, f8, (None, K, QUANT_BLOCK)), _is(xt_scale, f8, (xt.shape[0], K)),
-          min(dyt.shape[0], xt.shape[0]) >= quant_blocks(rows, p_end - p_begin), _is(grads, i64, (None,)),
-          grads.shape[0] >= p_end - p_begin)
+    dev, f8, _, i64, _ = _types()
+    _need(fn, rows >= 0 and _is_plan(ctx, plan, dev) and _is(dyt, dev, f8, None, N, QUANT_BLOCK) and _is(dyt_scale, dev, f8, dyt.shape[0], N)
+          and _is(xt, dev, f8, None, K, QUANT_BLOCK) and _is(xt_scale, dev, f8, xt.shape[0], K)
+          and min(dyt.shape[0], xt.shape[0]) >= quant_blocks(rows, p_end - p_begin) and _is(grads, dev, i64, None)
+          and grads.shape[0] >= p_end - p_begin)
     st = lib().ultraep_expert_wgrad(ctx.handle, _ptr(plan), _ptr(dyt), _ptr(dyt_scale), N, _ptr(xt), _ptr(xt_scale), K,
                                     p_begin, p_end, rows, _ptr(grads), int(accumulate), _stream(stream))
     _check(fn, st)
 
 
-def _grad_dtype(fn: str, dtype) -> int:
+def _grad_checks(fn: str, tensors, numels, n: int, dtype, sumsq) -> tuple:
+    """(current device, dtype code) of a call over gradient tensors."""
     import torch
-    _need(fn, dtype in (torch.float32, torch.bfloat16))
-    return int(dtype == torch.bfloat16)
+    dev, _, _, i64, _ = _types()
+    _need(fn, _is(tensors, dev, i64, None) and _is(numels, dev, i64, None) and tensors.shape[0] >= n
+          and numels.shape[0] >= n and _is(sumsq, dev, (torch.float64,), 1)
+          and (dtype is torch.float32 or dtype is torch.bfloat16))
+    return dev, int(dtype is torch.bfloat16)
 
 
 def ultraep_grad_sumsq(ctx: Context, tensors, numels, n: int, dtype, sumsq, workspace, accumulate: bool = False,
                        stream=None) -> None:
     """sumsq (fp64 [1]) = or += the squares of n tensors' elements (tensors, numels: int64 device tensors;
     workspace: GRAD_WORKSPACE_BYTES)."""
-    import torch
     fn = "ultraep_grad_sumsq"
-    i64 = _types()[2]
-    _need(fn, _is(tensors, i64, (None,)), _is(numels, i64, (None,)), min(tensors.shape[0], numels.shape[0]) >= n,
-          _is(sumsq, {torch.float64}, (1,)), workspace.is_cuda)
-    st = lib().ultraep_grad_sumsq(ctx.handle, _ptr(tensors), _ptr(numels), n, _grad_dtype(fn, dtype), _ptr(sumsq),
-                                  int(accumulate), _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                  _stream(stream))
+    dev, code = _grad_checks(fn, tensors, numels, n, dtype, sumsq)
+    _need(fn, workspace.get_device() == dev and workspace.is_contiguous())
+    st = lib().ultraep_grad_sumsq(ctx.handle, _ptr(tensors), _ptr(numels), n, code, _ptr(sumsq), int(accumulate),
+                                  _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
     _check(fn, st)
 
 
@@ -418,12 +435,11 @@ def ultraep_grad_clip(ctx: Context, tensors, numels, n: int, dtype, sumsq, max_n
     norm (fp32 [1], optional) receives the norm before."""
     import torch
     fn = "ultraep_grad_clip"
-    i64 = _types()[2]
-    _need(fn, _is(tensors, i64, (None,)), _is(numels, i64, (None,)), min(tensors.shape[0], numels.shape[0]) >= n,
-          _is(sumsq, {torch.float64}, (1,)), norm is None or _is(norm, {torch.float32}, (1,)),
-          out is None or (_is(out, i64, (None,)) and out.shape[0] >= n))
-    st = lib().ultraep_grad_clip(ctx.handle, _ptr(tensors), _ptr(numels), n, _grad_dtype(fn, dtype), _ptr(sumsq),
-                                 float(max_norm), _ptr(norm), _ptr(out), _stream(stream))
+    dev, code = _grad_checks(fn, tensors, numels, n, dtype, sumsq)
+    _need(fn, (norm is None or _is(norm, dev, (torch.float32,), 1))
+          and (out is None or (_is(out, dev, (torch.int64,), None) and out.shape[0] >= n)))
+    st = lib().ultraep_grad_clip(ctx.handle, _ptr(tensors), _ptr(numels), n, code, _ptr(sumsq), float(max_norm),
+                                 _ptr(norm), _ptr(out), _stream(stream))
     _check(fn, st)
 
 

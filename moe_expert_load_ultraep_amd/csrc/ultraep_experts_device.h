@@ -88,31 +88,47 @@ __device__ __forceinline__ RowTile find_row_tile(const int32_t* off, int32_t ne,
   }
 }
 
-// Exponent of a block whose largest finite magnitude has these float bits:
-// the smallest e >= -126 with amax <= 448 * 2^e = 1.75 * 2^(8 + e), 0 for a
-// block without a finite value other than zero.
+// Exponent of a block whose largest finite magnitude has these bf16 bits: the
+// smallest e >= -126 with amax <= 448 * 2^e = 1.75 * 2^(8 + e), 0 for a block
+// without a finite value other than zero.
 __device__ __forceinline__ int32_t block_exponent(uint32_t amax) {
-  const int32_t e = static_cast<int32_t>(amax >> 23) - 135 + ((amax & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  const int32_t e = static_cast<int32_t>(amax >> 7) - 135 + ((amax & 0x7Fu) > 0x60u ? 1 : 0);
   return amax == 0 ? 0 : max(e, -126);
 }
 
-// 2^-e for e in [-126, 120].
-__device__ __forceinline__ float inverse_scale(int32_t e) {
-  return __builtin_bit_cast(float, static_cast<uint32_t>(127 - e) << 23);
+// 2^e for e in [-126, 127].
+__device__ __forceinline__ float power_of_two(int32_t e) {
+  return __builtin_bit_cast(float, static_cast<uint32_t>(127 + e) << 23);
 }
 
-// Magnitude bits of a bf16 pair's low or high value as a float's; 0 when it is
-// not finite.  Magnitudes order as their bits do.
-__device__ __forceinline__ uint32_t finite_bits(uint32_t v) {
-  const uint32_t m = v & 0x7FFFFFFFu;
-  return m < 0x7F800000u ? m : 0u;
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+typedef int16_t i16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+// Magnitudes order as their bits do.  A block's largest is taken over all of
+// them, two at a time, and once more without the infinities and NaN where the
+// first answer is one (kNotFinite and above).
+constexpr uint32_t kNotFinite = 0x7F80;
+
+__device__ __forceinline__ uint32_t pair_max(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
 }
 
+template <bool FINITE>
+__device__ __forceinline__ uint32_t magnitudes(uint32_t v) {
+  const uint32_t m = v & 0x7FFF7FFFu;
+  if (!FINITE) return m;
+  const uint32_t lo = m & 0xFFFFu, hi = m >> 16;
+  return (lo < kNotFinite ? lo : 0u) | (hi < kNotFinite ? hi << 16 : 0u);
+}
+
+// Largest magnitude of eight bf16, as bf16 bits.
+template <bool FINITE>
 __device__ __forceinline__ uint32_t amax_of(const u32x4& x) {
   uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) m = max(m, max(finite_bits(x[i] << 16), finite_bits(x[i] & 0xFFFF0000u)));
-  return m;
+  for (int i = 0; i < 4; ++i) m = pair_max(m, magnitudes<FINITE>(x[i]));
+  return max(m & 0xFFFFu, m >> 16);
 }
 
 // Largest of 16 lanes (one aligned row), in every lane.
@@ -123,17 +139,25 @@ __device__ __forceinline__ uint32_t row16_max(uint32_t x) {
   return max(x, dpp<0x140>(x));
 }
 
-// Eight bf16 times a power of two, rounded to nearest even e4m3 (infinities
-// and NaN give NaN; nothing else is above 448).
-__device__ __forceinline__ u32x2 to_e4m3(const u32x4& x, float s) {
-  u32x2 y;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    int v = __builtin_amdgcn_cvt_pk_fp8_f32(bf16_lo(x[2 * i]) * s, bf16_hi(x[2 * i]) * s, 0, false);
-    v = __builtin_amdgcn_cvt_pk_fp8_f32(bf16_lo(x[2 * i + 1]) * s, bf16_hi(x[2 * i + 1]) * s, v, true);
-    y[i] = static_cast<uint32_t>(v);
-  }
-  return y;
+// Largest finite magnitude of the 16 lanes' values, as bf16 bits, in every lane.
+__device__ __forceinline__ uint32_t row16_amax(const u32x4& x) {
+  const uint32_t m = row16_max(amax_of<false>(x));
+  if (__builtin_expect(ballot(m >= kNotFinite) != 0, 0)) return row16_max(amax_of<true>(x));
+  return m;
+}
+
+// Two pairs of bf16 over a power of two, rounded to nearest even e4m3: the
+// conversion scales exactly (subnormals included), infinities and NaN give NaN
+// and nothing else is above 448.
+__device__ __forceinline__ uint32_t to_e4m3(uint32_t pair0, uint32_t pair1, float scale) {
+  i16x2 r = {0, 0};
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(bf16x2, pair0), scale, false);
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(bf16x2, pair1), scale, true);
+  return __builtin_bit_cast(uint32_t, r);
+}
+
+__device__ __forceinline__ u32x2 to_e4m3(const u32x4& x, float scale) {
+  return u32x2{to_e4m3(x[0], x[1], scale), to_e4m3(x[2], x[3], scale)};
 }
 
 }  // namespace

@@ -6,6 +6,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "ultraep_experts_device.h"
 #include "ultraep_internal.h"
@@ -51,10 +52,10 @@ __global__ __launch_bounds__(kQuantThreads) void quant_rows_kernel(
     const __amdgpu_buffer_rsrc_t src = row_rsrc(in.hidden + static_cast<int64_t>(max(tlo, 0)) * H,
                                                 tlo < 0 ? 0u : 2u * static_cast<uint32_t>(H));
     const u32x4 x = __builtin_amdgcn_raw_buffer_load_b128(src, ch * 2 * kRowChunk + lane * 16, 0, kNonTemporal);
-    const int32_t e = block_exponent(row16_max(amax_of(x)));
-    const u32x2 y = to_e4m3(x, inverse_scale(e));
+    const int32_t e = block_exponent(row16_amax(x));
+    const u32x2 y = to_e4m3(x, power_of_two(e));
     const __amdgpu_buffer_rsrc_t dst = row_rsrc(q + row * Hp, static_cast<uint32_t>(Hp));
-    __builtin_amdgcn_raw_buffer_store_b64(y, dst, ch * kRowChunk + lane * 8, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b64(y, dst, ch * kRowChunk + lane * 8, 0, kNonTemporal);
     uint32_t s = 0;
 #pragma unroll
     for (int b = 0; b < 4; ++b) s |= (readlane(static_cast<uint32_t>(e), 16 * b) + 127u) << (8 * b);
@@ -108,8 +109,8 @@ __global__ __launch_bounds__(kQuantThreads) void quant_cols_kernel(
     uint8_t* __restrict__ scale, uint8_t* __restrict__ qt, uint8_t* __restrict__ scale_t, int64_t cap,
     int32_t nblk, int32_t ncol) {
   __shared__ __align__(16) uint8_t s_tile[kQBlock * kQBlock];
-  __shared__ uint32_t s_max[16][kQBlock];
-  __shared__ float s_inv[kQBlock];
+  __shared__ u32x4 s_max[16][16];
+  __shared__ float s_scale[kQBlock];
   const int tid = threadIdx.x, c = tid & 15, g = tid >> 4;
   const int32_t seg0 = off[0];
   const int32_t Hp = q_pitch(H), Hs = s_pitch(H);
@@ -120,73 +121,75 @@ __global__ __launch_bounds__(kQuantThreads) void quant_cols_kernel(
     const int64_t row0 = o + static_cast<int64_t>(b - (o / kQBlock + p)) * kQBlock;
     const int32_t live = static_cast<int32_t>(min(static_cast<int64_t>(o1) - row0, static_cast<int64_t>(kQBlock)));
     if (live <= 0) continue;  // the same for the whole workgroup
-    const int32_t h0 = cb * kQBlock + 8 * c;
+    const int32_t h0 = cb * kQBlock + 8 * c, hc = min(h0, H - 8);
+    // every lane loads (a row that is not there: row 0) and unwanted values are
+    // cleared; stores go through resources that end with the block's rows
     u32x4 x[8];
-    int32_t tok[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = u32x4{0, 0, 0, 0};
+    if (in.hidden_rows > 0)
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int r = 8 * g + i;
-      tok[i] = r < live ? static_cast<int32_t>(source_row(in, seg0, row0 + r)) : -1;
-    }
+      const int32_t tok = static_cast<int32_t>(source_row(in, seg0, row0 + min(r, live - 1)));
+      x[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(in.hidden + static_cast<int64_t>(max(tok, 0)) * H + hc));
+      const uint32_t keep = r < live && tok >= 0 && h0 < H ? 0xFFFFFFFFu : 0u;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      x[i] = u32x4{0, 0, 0, 0};
-      if (tok[i] >= 0 && h0 < H)
-        x[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(in.hidden + static_cast<int64_t>(tok[i]) * H + h0));
+      for (int j = 0; j < 4; ++j) x[i][j] &= keep;
     }
     if (ROWS) {
+      const __amdgpu_buffer_rsrc_t to_q = row_rsrc(q + row0 * Hp, static_cast<uint32_t>(live) * static_cast<uint32_t>(Hp));
+      const __amdgpu_buffer_rsrc_t to_s = row_rsrc(scale + row0 * Hs, static_cast<uint32_t>(live) * static_cast<uint32_t>(Hs));
+      // one scale byte a row, and behind the last block the padding's
+      const bool pad = c > 0 && cb == ncol - 1 && cb + c < Hs;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int r = 8 * g + i;
-        const int32_t e = block_exponent(row16_max(amax_of(x[i])));
-        const u32x2 y = to_e4m3(x[i], inverse_scale(e));
-        if (r < live) {
-          *reinterpret_cast<u32x2*>(q + (row0 + r) * Hp + h0) = y;
-          if (c == 0) scale[(row0 + r) * Hs + cb] = static_cast<uint8_t>(e + 127);
-          if (cb == ncol - 1 && c > 0 && cb + c < Hs) scale[(row0 + r) * Hs + cb + c] = 127;
-        }
+        const int32_t e = block_exponent(row16_amax(x[i]));
+        __builtin_amdgcn_raw_buffer_store_b64(to_e4m3(x[i], power_of_two(e)), to_q, r * Hp + h0, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b8(static_cast<uint8_t>(c == 0 ? e + 127 : 127), to_s,
+                                             c == 0 || pad ? r * Hs + cb + c : 0x7FFFFFFF, 0, 0);
       }
     }
     // column maxima: over the thread's rows, then over the 16 row groups
-    uint32_t m[8];
+    int32_t e = 0;
+    const auto column_maxima = [&](auto finite) {
+      u32x4 m = {0, 0, 0, 0};
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m[j] = 0;
+      for (int i = 0; i < 8; ++i)
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        m[2 * j] = max(m[2 * j], finite_bits(x[i][j] << 16));
-        m[2 * j + 1] = max(m[2 * j + 1], finite_bits(x[i][j] & 0xFFFF0000u));
-      }
-    __syncthreads();  // the previous item's readers are done
-#pragma unroll
-    for (int j = 0; j < 8; ++j) s_max[g][8 * c + j] = m[j];
-    __syncthreads();
-    if (tid < kQBlock) {
+        for (int j = 0; j < 4; ++j) m[j] = pair_max(m[j], magnitudes<decltype(finite)::value>(x[i][j]));
+      __syncthreads();  // earlier readers are done
+      s_max[g][c] = m;
+      __syncthreads();
       uint32_t mm = 0;
+      if (tid < kQBlock) {
+        const uint16_t* col = reinterpret_cast<const uint16_t*>(s_max) + tid;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) mm = max(mm, s_max[i][tid]);
-      const int32_t e = block_exponent(mm);
-      s_inv[tid] = inverse_scale(e);
+        for (int i = 0; i < 16; ++i) mm = max(mm, static_cast<uint32_t>(col[i * kQBlock]));
+        e = block_exponent(mm);
+        s_scale[tid] = power_of_two(e);
+      }
+      return __syncthreads_or(mm >= kNotFinite) != 0;
+    };
+    if (column_maxima(std::false_type{})) column_maxima(std::true_type{});
+    if (tid < kQBlock) {
       const int32_t h = cb * kQBlock + tid;
       if (h < H) scale_t[static_cast<int64_t>(b) * H + h] = static_cast<uint8_t>(e + 127);
     }
-    __syncthreads();
     float sc[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sc[j] = s_inv[8 * c + j];
-    u32x2 a[8], bt[8];
+    for (int j = 0; j < 8; ++j) sc[j] = s_scale[8 * c + j];
+    // column j's rows in pairs, then in bytes
+    u32x2 bt[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t sel = j & 1 ? 0x07060302u : 0x05040100u;
+      uint32_t pair[4];
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const uint32_t v0 = x[i][2 * half], v1 = x[i][2 * half + 1];
-        int v = __builtin_amdgcn_cvt_pk_fp8_f32(bf16_lo(v0) * sc[4 * half], bf16_hi(v0) * sc[4 * half + 1], 0, false);
-        v = __builtin_amdgcn_cvt_pk_fp8_f32(bf16_lo(v1) * sc[4 * half + 2], bf16_hi(v1) * sc[4 * half + 3], v, true);
-        a[i][half] = static_cast<uint32_t>(v);
-      }
+      for (int i = 0; i < 4; ++i) pair[i] = __builtin_amdgcn_perm(x[2 * i + 1][j / 2], x[2 * i][j / 2], sel);
+      bt[j] = u32x2{to_e4m3(pair[0], pair[1], sc[j]), to_e4m3(pair[2], pair[3], sc[j])};
     }
-    transpose_bytes(a, bt);
     put_column_bytes(s_tile, c, g, bt);
     __syncthreads();
     const int32_t hcols = min(kQBlock, H - cb * kQBlock);
@@ -229,20 +232,24 @@ __global__ __launch_bounds__(kQuantThreads) void weight_quant_kernel(
         }
       }
     }
-    uint32_t m = 0;
+    const auto block_amax = [&](auto finite) {
+      uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, amax_of(x[i]));
-    m = wave_max(m);
-    __syncthreads();  // the previous item's readers are done
-    if ((tid & 63) == 0) s_max[tid >> 6] = m;
-    __syncthreads();
+      for (int i = 0; i < 8; ++i) m = max(m, amax_of<decltype(finite)::value>(x[i]));
+      m = wave_max(m);
+      __syncthreads();  // earlier readers are done
+      if ((tid & 63) == 0) s_max[tid >> 6] = m;
+      __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kQuantWaves; ++i) m = max(m, s_max[i]);
+      for (int i = 0; i < kQuantWaves; ++i) m = max(m, s_max[i]);
+      return m;
+    };
+    uint32_t m = block_amax(std::false_type{});
+    if (m >= kNotFinite) m = block_amax(std::true_type{});  // the same for the whole workgroup
     const int32_t e = block_exponent(m);
-    const float inv = inverse_scale(e);
     u32x2 a[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) a[i] = to_e4m3(x[i], inv);
+    for (int i = 0; i < 8; ++i) a[i] = to_e4m3(x[i], power_of_two(e));
     if (q != nullptr) {
       const int32_t Kp = q_pitch(K), Ks = s_pitch(K);
 #pragma unroll
