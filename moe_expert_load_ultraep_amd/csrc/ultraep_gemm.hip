@@ -66,39 +66,51 @@ struct BigOperand {
   int32_t last;
 };
 
-// A wave's 128 rows of A are read as 16-row fragments i = 0..7, fragment row m
-// being row 32 * (m / 4) + 4 * i + m % 4, so that a lane's accumulators
-// (fragment rows 4 * (l / 16) + r) are 32 consecutive rows: whole lines when
-// they are stored.  B's halves are the tile's rows 0..127 and 128..255, of which
-// a wave has 64 each as fragments 0..3 and 4..7 (b_row).
+// A wave reads its rows as 16-row fragments, and a lane's four accumulators are
+// rows 4 * (l / 16).. of A's.  So that four lanes hold 64 consecutive bytes of
+// an output row, the fragments of A are laid two into 32 rows where the output is
+// bf16 (PAIRS: fragment i, row m is row 32 * (i / 2) + 8 * (m / 4) + 4 * (i % 2) +
+// m % 4 of the wave's 128: eight values a lane, four lanes side by side), and one
+// into 16 where it is fp32.
 //
-// Half H of an operand's block is what the two waves along it read as
-// fragments 4H..4H+3, 64 rows each: row s of the half is this row of the tile.
-template <bool A, int H>
+// Half H of an operand's block is what the two waves along it read as fragments
+// 4H..4H+3, 64 rows each: row s of the half is this row of the tile. 
+template <bool PAIRS, int H>
 __device__ __forceinline__ int half_row(int s) {
-  return A ? 128 * (s >> 6) + 32 * ((s >> 4) & 3) + 16 * H + (s & 15) : 128 * H + s;
+  return PAIRS ? 128 * (s >> 6) + 64 * H + (s & 63) : 128 * H + s;
 }
 
-// Row m of B's fragment j of wave column wj.
+// LDS bytes from a half's fragment 0 to fragment i, and a lane's row of fragment 0.
+template <bool PAIRS>
+__device__ __forceinline__ constexpr int fragment_at(int i) {
+  return PAIRS ? (i >> 1) * 4096 + (i & 1) * 512 : i * 2048;
+}
+
+template <bool PAIRS>
+__device__ __forceinline__ int fragment_row(int m) {
+  return PAIRS ? 8 * (m >> 2) + (m & 3) : m;
+}
+
+// Row m of fragment j of wave wj along an operand without pairs.
 __device__ __forceinline__ int b_row(int wj, int j, int m) { return 128 * (j >> 2) + 64 * wj + 16 * (j & 3) + m; }
 
 // In LDS a row is eight 16-byte parts, part c at c ^ key(row).  64 banks are two
 // rows wide: an even and an odd row share a key, and the eight pairs of the
 // sixteen rows that are read together have different ones.
-template <bool A>
+template <bool PAIRS>
 __device__ __forceinline__ int part_key(int s) {
-  return A ? ((s >> 1) & 1) | (((s >> 4) & 3) << 1) : (s >> 1) & 7;
+  return PAIRS ? ((s >> 1) & 1) | (((s >> 3) & 3) << 1) : (s >> 1) & 7;
 }
 
 // Byte offsets of the four 16-byte parts that this lane loads of half H.
-template <bool A, int H>
+template <bool PAIRS, int H>
 __device__ __forceinline__ void load_offsets(const BigOperand& op, uint32_t (&off)[4]) {
   const int lane = lane_id(), wv = threadIdx.x >> 6;
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     const int s = wv * 32 + u * 8 + (lane >> 3);
-    off[u] = static_cast<uint32_t>(min(half_row<A, H>(s), op.last)) * op.row_pitch +
-             static_cast<uint32_t>(((lane & 7) ^ part_key<A>(s)) * 16);
+    off[u] = static_cast<uint32_t>(min(half_row<PAIRS, H>(s), op.last)) * op.row_pitch +
+             static_cast<uint32_t>(((lane & 7) ^ part_key<PAIRS>(s)) * 16);
   }
 }
 
@@ -165,19 +177,17 @@ __device__ __forceinline__ void product(f32x4& acc, const i32x8& a, const i32x8&
 __device__ __forceinline__ void products_done() { asm volatile("s_nop 15\n\ts_nop 3"); }
 
 // Fragment i of a half in LDS; at[h]: this lane's part h.
-template <int STRIDE>
+template <bool PAIRS>
 __device__ __forceinline__ i32x8 read_fragment(const uint8_t* lds, const int (&at)[2], int i) {
-  return __builtin_shufflevector(*reinterpret_cast<const i32x4*>(lds + at[0] + i * STRIDE),
-                                 *reinterpret_cast<const i32x4*>(lds + at[1] + i * STRIDE), 0, 1, 2, 3, 4, 5, 6, 7);
+  return __builtin_shufflevector(*reinterpret_cast<const i32x4*>(lds + at[0] + fragment_at<PAIRS>(i)),
+                                 *reinterpret_cast<const i32x4*>(lds + at[1] + fragment_at<PAIRS>(i)), 0, 1, 2, 3, 4, 5, 6, 7);
 }
-
-constexpr int kStrideA = 4 * 128, kStrideB = 16 * 128;  // bytes from a fragment's rows to the next one's
 
 // A quarter of the wave's products: fragments a[4] by b[4], with the reads of
 // the four fragments f of half `lds` and the loads of another half among them: a
 // load's issue takes long enough for the matrix unit to run dry when several
 // follow each other.
-template <int I0, int J0, int BYTE, int STRIDE>
+template <int I0, int J0, int BYTE, bool PAIRS>
 __device__ __forceinline__ void quadrant(const i32x8 (&a)[4], const i32x8 (&b)[4], int xa, const int (&xb)[8],
                                          f32x4 (&acc)[8][8], const uint8_t* lds, const int (&at)[2], i32x8 (&f)[4], const HalfLoad& load) {
 #pragma unroll
@@ -185,7 +195,7 @@ __device__ __forceinline__ void quadrant(const i32x8 (&a)[4], const i32x8 (&b)[4
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       product<BYTE>(acc[I0 + i][J0 + j], a[i], b[j], xa, xb[J0 + j]);
-      if (j == 0) f[i] = read_fragment<STRIDE>(lds, at, i);
+      if (j == 0) f[i] = read_fragment<PAIRS>(lds, at, i);
       if (j == 2) load.issue(i);
     }
 }
@@ -239,13 +249,13 @@ __device__ __forceinline__ void big_step(const BigOperand& a, const BigOperand& 
                                          ScaleWords& sn, f32x4 (&acc)[8][8]) {
   constexpr int X = U & 1, Y = 1 - X;
   meet<16>();
-  quadrant<0, 4 * X, U, kStrideB>(fal, fbx, sw.a, sw.b, acc, by, o.read_b, fby, HalfLoad(a, k + 2, blocks, o.a[0], alo));
-  quadrant<0, 4 * Y, U, kStrideA>(fal, fby, sw.a, sw.b, acc, ahi, o.read_a, fah, HalfLoad(b, k + 2, blocks, o.b[X], bx));
+  quadrant<0, 4 * X, U, false>(fal, fbx, sw.a, sw.b, acc, by, o.read_b, fby, HalfLoad(a, k + 2, blocks, o.a[0], alo));
+  quadrant<0, 4 * Y, U, true>(fal, fby, sw.a, sw.b, acc, ahi, o.read_a, fah, HalfLoad(b, k + 2, blocks, o.b[X], bx));
   meet<16>();
   if (U == 2) load_scales(ss, min(k + 2, blocks - 1) & ~3, sn);
-  quadrant<4, 4 * Y, U, kStrideA>(fah, fby, sw.a, sw.b, acc, next_alo, o.read_a, fal,
+  quadrant<4, 4 * Y, U, true>(fah, fby, sw.a, sw.b, acc, next_alo, o.read_a, fal,
                                   HalfLoad(b, k + 2, blocks, o.b[Y], by));
-  quadrant<4, 4 * X, U, kStrideB>(fah, fbx, sw.a, sw.b, acc, next_by, o.read_b, fby,
+  quadrant<4, 4 * X, U, false>(fah, fbx, sw.a, sw.b, acc, next_by, o.read_b, fby,
                                   HalfLoad(a, k + 2, blocks, o.a[1], ahi));
   if (U == 3) {
     sw = sn;
@@ -261,13 +271,13 @@ __device__ __forceinline__ void half_step(const BigOperand& a, const BigOperand&
                                           i32x8 (&fbn)[4], const ScaleSource& ss, ScaleWords& sw, ScaleWords& sn,
                                           f32x4 (&acc)[8][8]) {
   meet<12>();
-  quadrant<0, 0, U, kStrideA>(fal, fb, sw.a, sw.b, acc, ahi, o.read_a, fah, HalfLoad(a, k + 2, blocks, o.a[0], alo));
+  quadrant<0, 0, U, true>(fal, fb, sw.a, sw.b, acc, ahi, o.read_a, fah, HalfLoad(a, k + 2, blocks, o.a[0], alo));
   load_half(b, k + 2, blocks, o.b[0], bx);
   meet<12>();
   if (U == 2) load_scales(ss, min(k + 2, blocks - 1) & ~3, sn);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) fbn[i] = read_fragment<kStrideB>(next_bx, o.read_b, i);
-  quadrant<4, 0, U, kStrideA>(fah, fb, sw.a, sw.b, acc, next_alo, o.read_a, fal, HalfLoad(a, k + 2, blocks, o.a[1], ahi));
+  for (int i = 0; i < 4; ++i) fbn[i] = read_fragment<false>(next_bx, o.read_b, i);
+  quadrant<4, 0, U, true>(fah, fb, sw.a, sw.b, acc, next_alo, o.read_a, fal, HalfLoad(a, k + 2, blocks, o.a[1], ahi));
   if (U == 3) {
     sw = sn;
     products_done();
@@ -301,13 +311,13 @@ __device__ __forceinline__ bool usable(const uint8_t* w, const uint8_t* ws) {
 // Bound by the matrix units' rate at the clock they leave (about 2.0 GHz), and
 // next to that by the loads into LDS: alone, the products of a block of a full
 // tile take 1.0-1.3 us, its 64 KiB of loads 1.5 us, together 1.55 us.  Larger
-// tiles do not fit the registers.  32768 rows by 6 experts of 4096 x 7168: 781 us,
-// 2.46 PFLOP/s; 8192 x 8192 x 8192: 430 us, 2.56 PFLOP/s (a library's plain 8-bit
+// tiles do not fit the registers.  32768 rows by 6 experts of 4096 x 7168: 740-780
+// us, 2.5-2.6 PFLOP/s; 8192 x 8192 x 8192: 430 us, 2.56 PFLOP/s (a library's plain 8-bit
 // product reaches 2.71-2.78 there).  Measured and not kept: one workgroup a CU that
 // walks the tiles and loads the next one's blocks before it stores (829 us: the
 // hardware's dealing balances better); a barrier a quadrant (853 us against 875,
 // before the loads were spread); all of a half's loads at once (875 us against
-// 807); non-temporal stores (1009 us against 881).
+// 807).
 __global__ __launch_bounds__(kMmThreads, 1) void expert_gemm_big_kernel(GemmArgs g, int32_t ntile,
                                                                         int32_t unit) {
   __shared__ __align__(16) uint8_t a00[kHalfBytes], a01[kHalfBytes], a10[kHalfBytes], a11[kHalfBytes];
@@ -336,8 +346,8 @@ __global__ __launch_bounds__(kMmThreads, 1) void expert_gemm_big_kernel(GemmArgs
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int part = ((2 * kg + h) ^ (l16 >> 1)) * 16;
-    o.read_a[h] = (wi * 64 + 16 * (l16 >> 2) + (l16 & 3)) * 128 + part;
-    o.read_b[h] = (wj * 64 + l16) * 128 + part;
+    o.read_a[h] = (wi * 64 + fragment_row<true>(l16)) * 128 + part;
+    o.read_b[h] = (wj * 64 + fragment_row<false>(l16)) * 128 + part;
   }
   ScaleWords sw, sn;
   load_scales(ss, 0, sw);
@@ -348,19 +358,28 @@ __global__ __launch_bounds__(kMmThreads, 1) void expert_gemm_big_kernel(GemmArgs
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   i32x8 fal[4], fah[4], fb0[4], fb1[4];
+  // A fragment of rows at a time through the wave's own piece of LDS, so that a
+  // store covers 256 consecutive bytes of four rows and need not go by way of the
+  // caches (32768 rows by 4 experts of 4096 x 1536: 218 us; straight from the
+  // registers, 64 bytes of sixteen rows, 235).
+  uint8_t* const stage = wv == 0 ? a00 : wv == 1 ? a01 : wv == 2 ? a10 : a11;
   const auto store = [&](int j0, int j1) {
-    const int c = wi * 128 + 32 * kg;
+    meet<0>();  // LDS is free: the last loads (zeros) have arrived, the reads are done
+    const int c = wi * 128 + 8 * l16;
 #pragma unroll
     for (int j = j0; j < j1; ++j) {
-      const int r = b_row(wj, j, l16);
-      if (r < rows) {
-        u32x4* d = reinterpret_cast<u32x4*>(g.out + (rt.row0 + r) * g.N + n0 + c);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (c + 8 * i < cols)
-            d[i] = u32x4{pack_bf16(acc[2 * i][j][0], acc[2 * i][j][1]), pack_bf16(acc[2 * i][j][2], acc[2 * i][j][3]),
-                         pack_bf16(acc[2 * i + 1][j][0], acc[2 * i + 1][j][1]),
-                         pack_bf16(acc[2 * i + 1][j][2], acc[2 * i + 1][j][3])};
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<u32x4*>(stage + l16 * 272 + 64 * i + 16 * kg) =
+            u32x4{pack_bf16(acc[2 * i][j][0], acc[2 * i][j][1]), pack_bf16(acc[2 * i][j][2], acc[2 * i][j][3]),
+                  pack_bf16(acc[2 * i + 1][j][0], acc[2 * i + 1][j][1]),
+                  pack_bf16(acc[2 * i + 1][j][2], acc[2 * i + 1][j][3])};
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int r = b_row(wj, j, 4 * u + kg);
+        const u32x4 y = *reinterpret_cast<const u32x4*>(stage + (4 * u + kg) * 272 + 16 * l16);
+        if (r < rows && c < cols)
+          __builtin_nontemporal_store(y, reinterpret_cast<u32x4*>(g.out + (rt.row0 + r) * g.N + n0 + c));
       }
     }
   };
@@ -376,8 +395,8 @@ __global__ __launch_bounds__(kMmThreads, 1) void expert_gemm_big_kernel(GemmArgs
     meet<24>();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      fal[i] = read_fragment<kStrideA>(a00, o.read_a, i);
-      fb0[i] = read_fragment<kStrideB>(b00, o.read_b, i);
+      fal[i] = read_fragment<true>(a00, o.read_a, i);
+      fb0[i] = read_fragment<false>(b00, o.read_b, i);
     }
     for (int32_t k = 0; k < blocks; k += 4) {
       big_step<0>(a, b, o, k, blocks, a00, a01, b00, b01, a10, b11, fal, fah, fb0, fb1, ss, sw, sn, acc);
@@ -394,8 +413,8 @@ __global__ __launch_bounds__(kMmThreads, 1) void expert_gemm_big_kernel(GemmArgs
     meet<16>();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      fal[i] = read_fragment<kStrideA>(a00, o.read_a, i);
-      fb0[i] = read_fragment<kStrideB>(b00, o.read_b, i);
+      fal[i] = read_fragment<true>(a00, o.read_a, i);
+      fb0[i] = read_fragment<false>(b00, o.read_b, i);
     }
     for (int32_t k = 0; k < blocks; k += 4) {
       half_step<0>(a, b, o, k, blocks, a00, a01, b00, a10, b10, fal, fah, fb0, fb1, ss, sw, sn, acc);
@@ -405,7 +424,6 @@ __global__ __launch_bounds__(kMmThreads, 1) void expert_gemm_big_kernel(GemmArgs
     }
     store(0, 4);
   }
-  meet<0>();  // no load outlives the workgroup's LDS
 }
 
 // ------------------------------------------------------------------------
@@ -413,7 +431,7 @@ __global__ __launch_bounds__(kMmThreads, 1) void expert_gemm_big_kernel(GemmArgs
 // ------------------------------------------------------------------------
 constexpr int kThinWaves = 4;
 constexpr int kThinThreads = 64 * kThinWaves;
-constexpr int kThinRows = 16, kThinCols = 64;
+constexpr int kThinRows = 16, kThinCols = 32;
 
 // Fragment of 16 rows: lane's two 16-byte parts kg and kg + 4 of its row, so
 // that one load covers 64 bytes of each row in order.  Both operands take the
@@ -423,13 +441,14 @@ __device__ __forceinline__ i32x8 thin_fragment(const uint8_t* row) {
                                  4, 5, 6, 7);
 }
 
-// FN * 16 weight rows by NJ * 16 rows.  The four waves split the blocks of 128
+// 32 weight rows by 16 rows.  The four waves split the blocks of 128
 // (wave v takes v, v + 4, ...), every weight byte goes from memory to the
 // registers of the one wave that uses it, DEPTH blocks ahead, and the waves'
 // sums meet in LDS and are added in wave order.  Bound by HBM: 41 rows by 6
-// experts of 4096 x 7168 (177 MB) take 31 us, 5.7 TB/s.  Eight or sixteen waves a
-// tile take 34 and 38 us, loads two blocks ahead 40 (fewer waves fit), 128
-// columns a tile 39, 32 rows 37; non-temporal loads 46.
+// experts of 4096 x 7168 (177 MB) take 34 us, 5.2 TB/s, the rate of a large copy.
+// Two or eight waves a tile take 38 us with 64 columns, four 36; 128 columns a
+// tile 43; loads two blocks ahead are slower (fewer waves fit), as are
+// non-temporal loads (46 us).
 __global__ __launch_bounds__(kThinThreads) void expert_gemm_thin_kernel(GemmArgs g, int32_t ntile) {
   constexpr int FN = kThinCols / 16;
   __shared__ __align__(16) float s_sum[kThinWaves][kThinRows][kThinCols + 4];
@@ -530,16 +549,14 @@ struct WideTile {
   BigOperand a, b;
   const uint8_t *scale_a, *scale_b;  // scale bytes of the tile's rows, block 0
   int32_t pitch_a, pitch_b;          // scale bytes a block
-  int32_t row_a;                     // this lane's row of A's fragment 0
-  int32_t wj, l16;
+  int32_t wi, wj, l16;
   uint32_t off_a[2][4], off_b[2][4];
   int at_a[4], at_b[4];              // LDS offset of this lane's eight bytes g, in a half
 };
 
 // Eight bytes of fragment i; the fragments' rows lie in two halves.
-template <int STRIDE>
 __device__ __forceinline__ i32x2v read_raw(const uint8_t* lo, const uint8_t* hi, int at, int i) {
-  return *reinterpret_cast<const i32x2v*>((i < 4 ? lo : hi) + at + (i & 3) * STRIDE);
+  return *reinterpret_cast<const i32x2v*>((i < 4 ? lo : hi) + at + fragment_at<false>(i & 3));
 }
 
 __device__ __forceinline__ int scale_byte(const uint8_t* s, int32_t row, int32_t last) { return s[min(row, last)]; }
@@ -577,23 +594,34 @@ __device__ __forceinline__ void wide_block(const WideTile& t, WideState& w, int3
       if (j == 3) widen_half<1>(w.b[(g + 1) & 1][i], w.raw_b[n & 3], w.sb[i]);
       if (j == 4) {
         const int m = n + 5;
-        w.raw_a[m & 3] = m < 32 ? read_raw<kStrideA>(al, ah, t.at_a[(m >> 3) & 3], m & 7)
-                                : read_raw<kStrideA>(nal, nah, t.at_a[0], m & 7);
+        w.raw_a[m & 3] = m < 32 ? read_raw(al, ah, t.at_a[(m >> 3) & 3], m & 7)
+                                : read_raw(nal, nah, t.at_a[0], m & 7);
       }
       if (j == 5) {
         const int m = n + 4;  // widened at step m for g + 1
-        w.raw_b[m & 3] = m < 24 ? read_raw<kStrideB>(bl, bh, t.at_b[((m >> 3) + 1) & 3], m & 7)
-                                : read_raw<kStrideB>(nbl, nbh, t.at_b[((m >> 3) + 1) & 3], m & 7);
+        w.raw_b[m & 3] = m < 24 ? read_raw(bl, bh, t.at_b[((m >> 3) + 1) & 3], m & 7)
+                                : read_raw(nbl, nbh, t.at_b[((m >> 3) + 1) & 3], m & 7);
       }
       if (j == 6 || j == 7) {
         if (n >= 2 && n < 10) {
-          if (j == 6) w.na[n - 2] = scale_byte(sa, t.row_a + 4 * (n - 2), t.a.last);
+          if (j == 6) w.na[n - 2] = scale_byte(sa, b_row(t.wi, n - 2, t.l16), t.a.last);
           if (j == 7) w.nb[n - 2] = scale_byte(sb, b_row(t.wj, n - 2, t.l16), t.b.last);
         }
         if (n >= 20 && n < 24) (j == 6 ? load_bl : load_bh).issue(n - 20);
         if (n >= 27 && n < 31) (j == 6 ? load_al : load_ah).issue(n - 27);
       }
     }
+  }
+}
+
+// Four consecutive values of a gradient; vec: its address allows 16-byte accesses.
+__device__ __forceinline__ void put_gradient(float* d, f32x4 y, bool accumulate, bool vec) {
+  if (vec) {
+    if (accumulate) y += *reinterpret_cast<const f32x4*>(d);
+    __builtin_nontemporal_store(y, reinterpret_cast<f32x4*>(d));
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) d[e] = accumulate ? d[e] + y[e] : y[e];
   }
 }
 
@@ -611,7 +639,7 @@ __device__ __forceinline__ int32_t expert_of_rank(const int32_t* off, int32_t ne
   return __builtin_amdgcn_readfirstlane(lowest_lane(ballot(l < ne && before == rank)));
 }
 
-// grads[p][n][k]: A is x (a lane holds 32 consecutive k of a row n), B is dy.
+// grads[p][n][k]: A is x (a lane holds four consecutive k of a row n), B is dy.
 //
 // Bound by the bf16 products at the clock they leave.  32768 rows, 6 experts of
 // 4096 x 7168: 1352 us, 1.42 PFLOP/s (a library's plain bf16 product reaches 1.24
@@ -652,11 +680,11 @@ __global__ __launch_bounds__(kMmThreads, 1) void expert_wgrad_big_kernel(
     t.scale_b = dyt_scale + first * N + n0;
     t.pitch_a = K;
     t.pitch_b = N;
-    t.row_a = wi * 128 + 32 * (l16 >> 2) + (l16 & 3);
+    t.wi = wi;
     t.wj = wj;
     t.l16 = l16;
-    load_offsets<true, 0>(t.a, t.off_a[0]);
-    load_offsets<true, 1>(t.a, t.off_a[1]);
+    load_offsets<false, 0>(t.a, t.off_a[0]);
+    load_offsets<false, 1>(t.a, t.off_a[1]);
     load_offsets<false, 0>(t.b, t.off_b[0]);
     load_offsets<false, 1>(t.b, t.off_b[1]);
     // odd lanes of sixteen take the two eights of a part the other way round, so
@@ -664,13 +692,13 @@ __global__ __launch_bounds__(kMmThreads, 1) void expert_wgrad_big_kernel(
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
       const int part = ((2 * kg + (g >> 1)) ^ (l16 >> 1)) * 16 + ((g ^ kg) & 1) * 8;
-      t.at_a[g] = (wi * 64 + 16 * (l16 >> 2) + (l16 & 3)) * 128 + part;
+      t.at_a[g] = (wi * 64 + l16) * 128 + part;
       t.at_b[g] = (wj * 64 + l16) * 128 + part;
     }
     WideState w;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      w.sa[j] = scale_of(scale_byte(t.scale_a, t.row_a + 4 * j, t.a.last));
+      w.sa[j] = scale_of(scale_byte(t.scale_a, b_row(wi, j, l16), t.a.last));
       w.sb[j] = scale_of(scale_byte(t.scale_b, b_row(wj, j, l16), t.b.last));
     }
 #pragma unroll
@@ -686,17 +714,17 @@ __global__ __launch_bounds__(kMmThreads, 1) void expert_wgrad_big_kernel(
     meet<16>();
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const i32x2v raw = read_raw<kStrideB>(b00, b01, t.at_b[0], j);
+      const i32x2v raw = read_raw(b00, b01, t.at_b[0], j);
       widen_half<0>(w.b[0][j], raw, w.sb[j]);
       widen_half<1>(w.b[0][j], raw, w.sb[j]);
     }
-    const i32x2v raw = read_raw<kStrideA>(a00, a01, t.at_a[0], 0);
+    const i32x2v raw = read_raw(a00, a01, t.at_a[0], 0);
     widen_half<0>(w.a[0], raw, w.sa[0]);
     widen_half<1>(w.a[0], raw, w.sa[0]);
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
-      w.raw_a[(m + 1) & 3] = read_raw<kStrideA>(a00, a01, t.at_a[0], m + 1);
-      w.raw_b[m] = read_raw<kStrideB>(b00, b01, t.at_b[1], m);
+      w.raw_a[(m + 1) & 3] = read_raw(a00, a01, t.at_a[0], m + 1);
+      w.raw_b[m] = read_raw(b00, b01, t.at_b[1], m);
     }
     asm volatile("s_nop 1");
     for (int32_t k = 0; k < blocks; k += 2) {
@@ -706,26 +734,23 @@ __global__ __launch_bounds__(kMmThreads, 1) void expert_wgrad_big_kernel(
     }
   }
   const bool vec = (reinterpret_cast<uintptr_t>(out) & 15) == 0;
-  const int c = wi * 128 + 32 * kg;
+  // a fragment of rows at a time through the wave's own piece of LDS, so that a
+  // store covers 256 consecutive bytes four times (4 experts of 1536 x 5120 from
+  // 2999 rows: 65 us; straight from the registers, 64 bytes of sixteen rows, 76)
+  uint8_t* const stage = wv == 0 ? a00 : wv == 1 ? a01 : wv == 2 ? a10 : a11;
+  const int c = 128 * ((lane >> 4) & 1) + 64 * wi + 4 * l16;
+  meet<0>();  // LDS is free: the last loads (zeros) have arrived, the reads are done
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const int r = b_row(wj, j, l16);
-    if (r >= rows) continue;
-    float* d = out + static_cast<int64_t>(n0 + r) * K + k0 + c;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (c + 4 * i >= cols) continue;
-      f32x4 y = acc[i][j];
-      if (vec) {
-        if (accumulate) y += *reinterpret_cast<const f32x4*>(d + 4 * i);
-        *reinterpret_cast<f32x4*>(d + 4 * i) = y;
-      } else {
+    for (int i = 0; i < 8; ++i) *reinterpret_cast<f32x4*>(stage + l16 * 528 + 64 * i + 16 * kg) = acc[i][j];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) d[4 * i + e] = accumulate ? d[4 * i + e] + y[e] : y[e];
-      }
+    for (int u = 0; u < 8; ++u) {
+      const int m = 2 * u + (lane >> 5), r = b_row(wj, j, m);
+      const f32x4 y = *reinterpret_cast<const f32x4*>(stage + m * 528 + 16 * (lane & 31));
+      if (r < rows && c < cols) put_gradient(out + static_cast<int64_t>(n0 + r) * K + k0 + c, y, accumulate, vec);
     }
   }
-  meet<0>();  // no load outlives the workgroup's LDS
 }
 
 uint32_t mm_grid(int64_t tiles) { return static_cast<uint32_t>(tiles < (1 << 20) ? tiles : (1 << 20)); }

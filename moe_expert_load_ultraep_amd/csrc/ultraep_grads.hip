@@ -3,11 +3,14 @@
 // them.
 //
 // Both walk the tensors' chunks of kGradBytes: a workgroup scans the tensors'
-// chunk counts into LDS once and takes one contiguous share of all chunks, so
-// tensors of any sizes spread evenly and the order of every sum depends on the
-// sizes alone.  HBM-streaming; the squares are added in fp64 (the vector units
-// do fp64 at the fp32 rate of one lane, far above what HBM feeds them), so no
-// square overflows and long sums lose nothing.
+// chunk counts into LDS once and takes every gridDim-th chunk, so tensors of any
+// sizes spread evenly, neighbouring chunks are read at one time, and the order of
+// every sum depends on the sizes alone.  Bound by HBM: 4e8 fp32 elements, read
+// twice and written once (4.8 GB), take 915 us, 5.2 TB/s, the rate of a large
+// copy.  One contiguous share a workgroup took 977 us, ordinary instead of
+// non-temporal accesses 930, two vectors in flight 934, eight 1002 (fewer waves
+// fit), half as many workgroups 967.  The squares are added in fp64, whose cost
+// does not show, so no square overflows and long sums lose nothing.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -24,17 +27,49 @@ constexpr int kGradVecs = 4;                                 // 16-byte vectors 
 constexpr int kGradBytes = kGradThreads * kGradVecs * 16;    // bytes of a chunk
 constexpr int kGradBlocks = ULTRAEP_GRAD_WORKSPACE_BYTES / 8;  // partial sums
 
-// Vectors at any alignment of their elements.
+// Vectors at any alignment of their elements, in global memory (addresses from
+// a table would otherwise be loaded as generic ones).
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+typedef __attribute__((address_space(1))) u32x4_any global_vec;
+typedef __attribute__((address_space(1))) uint16_t global_u16;
+typedef __attribute__((address_space(1))) float global_f32;
 
-struct Share {
-  int64_t begin, end;  // chunks of this workgroup
-  int32_t tensor;      // the tensor `begin` lies in
+__device__ __forceinline__ u32x4 load_vec(uintptr_t p) {
+  return __builtin_nontemporal_load(reinterpret_cast<const global_vec*>(p));
+}
+__device__ __forceinline__ void store_vec(uintptr_t p, const u32x4& v) {
+  __builtin_nontemporal_store(v, reinterpret_cast<global_vec*>(p));
+}
+
+// The workgroup's walk over the chunks: first[t] is the number of chunks before
+// tensor t, `total` the number of all.
+struct Walk {
+  const void* const* tensors;
+  const int64_t* numels;
+  int32_t n;
+  const int64_t* first;
+  int64_t total;
 };
 
-// first[t]: chunks of the tensors before t.  Returns the workgroup's share.
-__device__ Share grad_share(const void* const* tensors, const int64_t* numels, int32_t n, int32_t per_chunk,
-                            int64_t* first) {
+struct Chunk {
+  uintptr_t p;     // its first element
+  int64_t len;     // elements
+  int64_t at;      // elements of the tensor before it
+  int32_t tensor;
+};
+
+// Chunk c < total, at or behind `from`'s tensor.
+__device__ __forceinline__ Chunk chunk_at(const Walk& w, int64_t c, int32_t from, int32_t per_chunk, int32_t size) {
+  Chunk x;
+  x.tensor = from;
+  while (x.tensor + 1 < w.n && w.first[x.tensor + 1] <= c) ++x.tensor;
+  x.at = (c - w.first[x.tensor]) * per_chunk;
+  x.len = min(w.numels[x.tensor] - x.at, static_cast<int64_t>(per_chunk));
+  x.p = reinterpret_cast<uintptr_t>(w.tensors[x.tensor]) + x.at * size;
+  return x;
+}
+
+__device__ Walk grad_walk(const void* const* tensors, const int64_t* numels, int32_t n, int32_t per_chunk, int64_t* first) {
   __shared__ int64_t s_wave[kGradThreads / 64];
   const int tid = threadIdx.x, lane = lane_id(), wv = tid >> 6;
   const int32_t each = (n + kGradThreads - 1) / kGradThreads;
@@ -61,17 +96,7 @@ __device__ Share grad_share(const void* const* tensors, const int64_t* numels, i
   }
   for (int32_t t = t0; t < t1; ++t) first[t] += before;
   __syncthreads();
-  Share sh;
-  const int64_t each_wg = (total + gridDim.x - 1) / gridDim.x;
-  sh.begin = min(each_wg * blockIdx.x, total);
-  sh.end = min(sh.begin + each_wg, total);
-  int32_t lo = 0, hi = n;  // last tensor whose first chunk is at or before begin
-  while (hi - lo > 1) {
-    const int32_t mid = (lo + hi) >> 1;
-    if (first[mid] <= sh.begin) lo = mid; else hi = mid;
-  }
-  sh.tensor = lo;
-  return sh;
+  return Walk{tensors, numels, n, first, total};
 }
 
 __device__ __forceinline__ float f32_of(uint32_t bits) { return __builtin_bit_cast(float, bits); }
@@ -117,27 +142,27 @@ __global__ __launch_bounds__(kGradThreads) void grad_sumsq_kernel(const void* co
                                                                   const int64_t* __restrict__ numels, int32_t n,
                                                                   double* __restrict__ partial) {
   extern __shared__ int64_t s_first[];
-  constexpr int kVec = BF16 ? 8 : 4, kChunk = kGradBytes / (BF16 ? 2 : 4);
-  const Share sh = grad_share(tensors, numels, n, kChunk, s_first);
+  constexpr int kSize = BF16 ? 2 : 4, kVec = 16 / kSize, kChunk = kGradBytes / kSize;
+  const Walk w = grad_walk(tensors, numels, n, kChunk, s_first);
   double acc = 0.0;
-  int32_t t = sh.tensor;
-  for (int64_t c = sh.begin; c < sh.end; ++c) {
-    while (t + 1 < n && s_first[t + 1] <= c) ++t;
-    const int64_t at = (c - s_first[t]) * kChunk, len = min(numels[t] - at, static_cast<int64_t>(kChunk));
-    const char* p = static_cast<const char*>(tensors[t]) + at * (BF16 ? 2 : 4);
+  Chunk x, next;
+  if (blockIdx.x < w.total) next = chunk_at(w, blockIdx.x, 0, kChunk, kSize);
+  for (int64_t c = blockIdx.x; c < w.total; c += gridDim.x) {
+    x = next;
     u32x4 v[kGradVecs];
 #pragma unroll
     for (int u = 0; u < kGradVecs; ++u) {
       const int i = (u * kGradThreads + static_cast<int>(threadIdx.x)) * kVec;
       v[u] = u32x4{0, 0, 0, 0};
-      if (i + kVec <= len) v[u] = *reinterpret_cast<const u32x4_any*>(p + i * (BF16 ? 2 : 4));
+      if (i + kVec <= x.len) v[u] = load_vec(x.p + i * kSize);
     }
+    if (c + gridDim.x < w.total) next = chunk_at(w, c + gridDim.x, x.tensor, kChunk, kSize);
 #pragma unroll
     for (int u = 0; u < kGradVecs; ++u) acc += squares<BF16>(v[u]);
-    const int rest = static_cast<int>(len % kVec);  // values behind the last whole vector
+    const int rest = static_cast<int>(x.len % kVec);  // values behind the last whole vector
     if (static_cast<int>(threadIdx.x) < rest) {
-      const int64_t i = len - rest + threadIdx.x;
-      acc += square(BF16 ? bf16_lo(reinterpret_cast<const uint16_t*>(p)[i]) : reinterpret_cast<const float*>(p)[i]);
+      const int64_t i = x.len - rest + threadIdx.x;
+      acc += square(BF16 ? bf16_lo(reinterpret_cast<const global_u16*>(x.p)[i]) : reinterpret_cast<const global_f32*>(x.p)[i]);
     }
   }
   const double s = block_sum_f64(acc);
@@ -158,45 +183,45 @@ __global__ __launch_bounds__(kGradThreads) void grad_clip_kernel(const void* con
                                                                  const double* __restrict__ sumsq, double max_norm,
                                                                  float* __restrict__ norm_out, void* const* __restrict__ out) {
   extern __shared__ int64_t s_first[];
-  constexpr int kVec = BF16 ? 8 : 4, kChunk = kGradBytes / (BF16 ? 2 : 4), kSize = BF16 ? 2 : 4;
+  constexpr int kSize = BF16 ? 2 : 4, kVec = 16 / kSize, kChunk = kGradBytes / kSize;
   const double norm = sqrt(*sumsq), ratio = max_norm / (norm + 1e-6);
   const double coef = ratio >= 1.0 ? 1.0 : ratio;  // NaN stays NaN; fp64, since a huge norm's factor is below fp32's range
   if (blockIdx.x == 0 && threadIdx.x == 0 && norm_out != nullptr) *norm_out = static_cast<float>(norm);
   if (coef == 1.0 && out == nullptr) return;
-  const Share sh = grad_share(tensors, numels, n, kChunk, s_first);
-  int32_t t = sh.tensor;
-  for (int64_t c = sh.begin; c < sh.end; ++c) {
-    while (t + 1 < n && s_first[t + 1] <= c) ++t;
-    const int64_t at = (c - s_first[t]) * kChunk, len = min(numels[t] - at, static_cast<int64_t>(kChunk));
-    const char* p = static_cast<const char*>(tensors[t]) + at * kSize;
-    void* to = out == nullptr ? nullptr : out[t];
-    char* d = to == nullptr ? const_cast<char*>(p) : static_cast<char*>(to) + at * kSize;
-    if (coef == 1.0 && d == p) continue;
+  const Walk w = grad_walk(tensors, numels, n, kChunk, s_first);
+  Chunk x, next;
+  if (blockIdx.x < w.total) next = chunk_at(w, blockIdx.x, 0, kChunk, kSize);
+  for (int64_t c = blockIdx.x; c < w.total; c += gridDim.x) {
+    x = next;
     u32x4 v[kGradVecs];
 #pragma unroll
     for (int u = 0; u < kGradVecs; ++u) {
       const int i = (u * kGradThreads + static_cast<int>(threadIdx.x)) * kVec;
-      if (i + kVec <= len) v[u] = *reinterpret_cast<const u32x4_any*>(p + i * kSize);
+      if (i + kVec <= x.len) v[u] = load_vec(x.p + i * kSize);
     }
+    const uintptr_t to = out == nullptr ? 0 : reinterpret_cast<uintptr_t>(out[x.tensor]);
+    const uintptr_t d = to == 0 ? x.p : to + x.at * kSize;
+    if (c + gridDim.x < w.total) next = chunk_at(w, c + gridDim.x, x.tensor, kChunk, kSize);
+    if (coef == 1.0 && d == x.p) continue;
 #pragma unroll
     for (int u = 0; u < kGradVecs; ++u) {
       const int i = (u * kGradThreads + static_cast<int>(threadIdx.x)) * kVec;
-      if (i + kVec > len) continue;
+      if (i + kVec > x.len) continue;
       u32x4 y;
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         y[j] = BF16 ? pack_bf16(scaled(coef, bf16_lo(v[u][j])), scaled(coef, bf16_hi(v[u][j])))
                     : bits_of(scaled(coef, f32_of(v[u][j])));
-      *reinterpret_cast<u32x4_any*>(d + i * kSize) = y;
+      store_vec(d + i * kSize, y);
     }
-    const int rest = static_cast<int>(len % kVec);
+    const int rest = static_cast<int>(x.len % kVec);
     if (static_cast<int>(threadIdx.x) < rest) {
-      const int64_t i = len - rest + threadIdx.x;
+      const int64_t i = x.len - rest + threadIdx.x;
       if (BF16)
-        reinterpret_cast<uint16_t*>(d)[i] =
-            static_cast<uint16_t>(pack_bf16(scaled(coef, bf16_lo(reinterpret_cast<const uint16_t*>(p)[i])), 0.f));
+        reinterpret_cast<global_u16*>(d)[i] =
+            static_cast<uint16_t>(pack_bf16(scaled(coef, bf16_lo(reinterpret_cast<const global_u16*>(x.p)[i])), 0.f));
       else
-        reinterpret_cast<float*>(d)[i] = scaled(coef, reinterpret_cast<const float*>(p)[i]);
+        reinterpret_cast<global_f32*>(d)[i] = scaled(coef, reinterpret_cast<const global_f32*>(x.p)[i]);
     }
   }
 }
