@@ -131,13 +131,13 @@ int ultraep_expert_gemm(const ultraep_ctx* ctx, const void* plan, const uint8_t*
  * In:  dyt, dyt_scale (N columns) and xt, xt_scale (K columns): both in the
  *      columns form, capacity_rows / 128 + p_end - p_begin blocks; grads:
  *      DEVICE array of p_end - p_begin device pointers to fp32 [N][K] (any
- *      alignment of four bytes; a NULL entry is skipped).
+ *      alignment of four bytes; a NULL entry is skipped; no two may overlap).
  * Out: the gradients, added to with accumulate = 1, else overwritten (zeros for
  *      an expert without rows).
  * Errors: EINVAL (null pointers, N <= 0, K <= 0, bad range, capacity_rows < 0,
  *      accumulate not 0 or 1); EUNSUPPORTED (N % 8 or K % 8 != 0, N or K >
- *      2^20, capacity_rows >= 2^31, dyt or xt not 16-byte, scales not 8-byte,
- *      the table not 8-byte aligned). */
+ *      2^20, capacity_rows >= 2^31, more than 2^23 tiles of 256 x 256, dyt or xt
+ *      not 16-byte, the table not 8-byte aligned). */
 int ultraep_expert_wgrad(const ultraep_ctx* ctx, const void* plan, const uint8_t* dyt,
                          const uint8_t* dyt_scale, int32_t N, const uint8_t* xt,
                          const uint8_t* xt_scale, int32_t K, int32_t p_begin, int32_t p_end,
@@ -167,7 +167,8 @@ int ultraep_grad_sumsq(const ultraep_ctx* ctx, const void* const* tensors, const
  * In:  tensors, numels, n, dtype as above, sumsq from ultraep_grad_sumsq.
  * Out: the tensors, in place (out NULL) or in the tensors that out, a DEVICE
  *      array of n device pointers, names (a NULL entry: that tensor in place);
- *      norm: one fp32, or NULL.
+ *      what is written may overlap nothing else that the call reads or writes (a
+ *      tensor named twice would be scaled twice); norm: one fp32, or NULL.
  * Errors: EINVAL (null pointers, n < 0, dtype, max_norm negative or NaN);
  *      EUNSUPPORTED (n > ULTRAEP_MAX_GRAD_TENSORS, tables or sumsq not 8-byte,
  *      norm not 4-byte aligned). */

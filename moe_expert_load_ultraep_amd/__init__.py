@@ -300,26 +300,32 @@ def pointer_table(tensors, device="cuda"):
     return torch.tensor([0 if t is None else t.data_ptr() for t in tensors], dtype=torch.int64).to(device)
 
 
-_TYPES = None
+_F8 = _F16 = _I64 = _I32 = _device = None
 
 
 def _types():
-    """(current device, e4m3 types, bf16 types, int64, int32): what a call checks its buffers against."""
-    global _TYPES
+    """The types a call's buffers may have, and the current device's index, found once torch is in use."""
+    global _F8, _F16, _I64, _I32, _device
     import torch
-    if _TYPES is None:
-        _TYPES = (frozenset({torch.uint8, torch.float8_e4m3fn}),
-                  frozenset({torch.bfloat16, torch.int16, torch.uint16}), frozenset({torch.int64}),
-                  frozenset({torch.int32}))
-    return (torch.cuda.current_device() if torch.cuda.is_initialized() else None, *_TYPES)
+    _F8 = (torch.uint8, torch.float8_e4m3fn)
+    _F16 = (torch.bfloat16, torch.int16, torch.uint16)
+    _I64, _I32 = (torch.int64,), (torch.int32,)
+    _device = lambda: torch.cuda.current_device() if torch.cuda.is_initialized() else None  # noqa: E731
+
+
+def _here():
+    """Index of the current device (None where there is none)."""
+    if _device is None:
+        _types()
+    return _device()
 
 
 def _is(t, dev, dtypes, *shape) -> bool:
     """A contiguous tensor of the current device with one of the types and this shape; the first extent may be
     None (any)."""
     s = t.shape
-    return (t.get_device() == dev and t.dtype in dtypes and len(s) == len(shape)
-            and (s == shape if shape[0] is not None else s[1:] == shape[1:]) and t.is_contiguous())
+    return (t.get_device() == dev and t.dtype in dtypes and t.is_contiguous()
+            and (s == shape if shape[0] is not None else len(s) == len(shape) and s[1:] == shape[1:]))
 
 
 def _is_plan(ctx, plan, dev) -> bool:
@@ -340,20 +346,20 @@ def ultraep_permute_quant(ctx: Context, plan, inv, k: int, hidden, p_begin: int,
     qt [blocks, H, 128] with qt_scale [blocks, H] the columns form.  `rows` is the segment's capacity,
     by default q's rows (with qt alone it has to be given)."""
     fn = "ultraep_permute_quant"
-    dev, f8, f16, _, i32 = _types()
+    dev = _here()
     _need(fn, (q is None) == (q_scale is None) and (qt is None) == (qt_scale is None) and not (q is None and qt is None)
           and hidden.dim() == 2 and (rows is not None or q is not None))
     H = hidden.shape[1]
     if rows is None:
         rows = q.shape[0]
     blocks = 0
-    _need(fn, _is_plan(ctx, plan, dev) and _is(hidden, dev, f16, None, H) and (inv is None or _is(inv, dev, i32, None)))
+    _need(fn, _is_plan(ctx, plan, dev) and _is(hidden, dev, _F16, None, H) and (inv is None or _is(inv, dev, _I32, None)))
     if q is not None:
-        _need(fn, _is(q, dev, f8, None, quant_pitch(H)) and _is(q_scale, dev, f8, q.shape[0], quant_scale_pitch(H))
+        _need(fn, _is(q, dev, _F8, None, quant_pitch(H)) and _is(q_scale, dev, _F8, q.shape[0], quant_scale_pitch(H))
               and rows <= q.shape[0])
     if qt is not None:
         blocks = qt.shape[0]
-        _need(fn, _is(qt, dev, f8, None, H, QUANT_BLOCK) and _is(qt_scale, dev, f8, blocks, H))
+        _need(fn, _is(qt, dev, _F8, None, H, QUANT_BLOCK) and _is(qt_scale, dev, _F8, blocks, H))
     st = lib().ultraep_permute_quant(ctx.handle, _ptr(plan), _ptr(inv), k, _ptr(hidden), hidden.shape[0], H, p_begin,
                                      p_end, _ptr(q), _ptr(q_scale), _ptr(qt), _ptr(qt_scale), rows, blocks,
                                      _stream(stream))
@@ -365,13 +371,13 @@ def ultraep_weight_quant(ctx: Context, weights, n: int, N: int, K: int, q=None, 
     """weights: int64 device tensor [n] of pointers to bf16 [N, K]; q [n, N, quant_pitch(K)] with q_scale
     [n, ceil(N/128), quant_scale_pitch(K)], and the transposes' qt [n, K, quant_pitch(N)] with qt_scale."""
     fn = "ultraep_weight_quant"
-    dev, f8, _, i64, _ = _types()
+    dev = _here()
     _need(fn, (q is None) == (q_scale is None) and (qt is None) == (qt_scale is None)
-          and _is(weights, dev, i64, None) and weights.shape[0] >= n)
+          and _is(weights, dev, _I64, None) and weights.shape[0] >= n)
     for a, b, x, xs in ((N, K, q, q_scale), (K, N, qt, qt_scale)):
         if x is not None:
-            _need(fn, _is(x, dev, f8, None, a, quant_pitch(b))
-                  and _is(xs, dev, f8, None, quant_pitch(a) // QUANT_BLOCK, quant_scale_pitch(b))
+            _need(fn, _is(x, dev, _F8, None, a, quant_pitch(b))
+                  and _is(xs, dev, _F8, None, quant_pitch(a) // QUANT_BLOCK, quant_scale_pitch(b))
                   and x.shape[0] >= n and xs.shape[0] >= n)
     st = lib().ultraep_weight_quant(ctx.handle, _ptr(weights), n, N, K, _ptr(q), _ptr(q_scale), _ptr(qt),
                                     _ptr(qt_scale), _stream(stream))
@@ -384,10 +390,10 @@ def ultraep_expert_gemm(ctx: Context, plan, q, q_scale, K: int, w, w_scale, N: i
 
     w, w_scale: int64 device tensors [p_end - p_begin] of pointers to the quantised weights and scales."""
     fn = "ultraep_expert_gemm"
-    dev, f8, f16, i64, _ = _types()
-    _need(fn, _is_plan(ctx, plan, dev) and _is(q, dev, f8, None, quant_pitch(K)) and _is(q_scale, dev, f8, q.shape[0], quant_scale_pitch(K))
-          and _is(w, dev, i64, None) and _is(w_scale, dev, i64, None) and w.shape[0] >= p_end - p_begin
-          and w_scale.shape[0] >= p_end - p_begin and _is(out, dev, f16, None, N))
+    dev = _here()
+    _need(fn, _is_plan(ctx, plan, dev) and _is(q, dev, _F8, None, quant_pitch(K)) and _is(q_scale, dev, _F8, q.shape[0], quant_scale_pitch(K))
+          and _is(w, dev, _I64, None) and _is(w_scale, dev, _I64, None) and w.shape[0] >= p_end - p_begin
+          and w_scale.shape[0] >= p_end - p_begin and _is(out, dev, _F16, None, N))
     st = lib().ultraep_expert_gemm(ctx.handle, _ptr(plan), _ptr(q), _ptr(q_scale), K, _ptr(w), _ptr(w_scale), N,
                                    p_begin, p_end, _ptr(out), min(out.shape[0], q.shape[0]), _stream(stream))
     _check(fn, st)
@@ -397,10 +403,10 @@ def ultraep_expert_wgrad(ctx: Context, plan, dyt, dyt_scale, N: int, xt, xt_scal
                          rows: int, grads, accumulate: bool = False, stream=None) -> None:
     """grads: int64 device tensor [p_end - p_begin] of pointers to fp32 [N, K]; rows: the segment's capacity."""
     fn = "ultraep_expert_wgrad"
-    dev, f8, _, i64, _ = _types()
-    _need(fn, rows >= 0 and _is_plan(ctx, plan, dev) and _is(dyt, dev, f8, None, N, QUANT_BLOCK) and _is(dyt_scale, dev, f8, dyt.shape[0], N)
-          and _is(xt, dev, f8, None, K, QUANT_BLOCK) and _is(xt_scale, dev, f8, xt.shape[0], K)
-          and min(dyt.shape[0], xt.shape[0]) >= quant_blocks(rows, p_end - p_begin) and _is(grads, dev, i64, None)
+    dev = _here()
+    _need(fn, rows >= 0 and _is_plan(ctx, plan, dev) and _is(dyt, dev, _F8, None, N, QUANT_BLOCK) and _is(dyt_scale, dev, _F8, dyt.shape[0], N)
+          and _is(xt, dev, _F8, None, K, QUANT_BLOCK) and _is(xt_scale, dev, _F8, xt.shape[0], K)
+          and min(dyt.shape[0], xt.shape[0]) >= quant_blocks(rows, p_end - p_begin) and _is(grads, dev, _I64, None)
           and grads.shape[0] >= p_end - p_begin)
     st = lib().ultraep_expert_wgrad(ctx.handle, _ptr(plan), _ptr(dyt), _ptr(dyt_scale), N, _ptr(xt), _ptr(xt_scale), K,
                                     p_begin, p_end, rows, _ptr(grads), int(accumulate), _stream(stream))
@@ -410,8 +416,8 @@ def ultraep_expert_wgrad(ctx: Context, plan, dyt, dyt_scale, N: int, xt, xt_scal
 def _grad_checks(fn: str, tensors, numels, n: int, dtype, sumsq) -> tuple:
     """(current device, dtype code) of a call over gradient tensors."""
     import torch
-    dev, _, _, i64, _ = _types()
-    _need(fn, _is(tensors, dev, i64, None) and _is(numels, dev, i64, None) and tensors.shape[0] >= n
+    dev = _here()
+    _need(fn, _is(tensors, dev, _I64, None) and _is(numels, dev, _I64, None) and tensors.shape[0] >= n
           and numels.shape[0] >= n and _is(sumsq, dev, (torch.float64,), 1)
           and (dtype is torch.float32 or dtype is torch.bfloat16))
     return dev, int(dtype is torch.bfloat16)

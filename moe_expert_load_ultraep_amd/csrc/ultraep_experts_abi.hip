@@ -91,8 +91,8 @@ int ultraep_expert_wgrad(const ultraep_ctx* ctx, const void* plan, const uint8_t
   if (N <= 0 || K <= 0 || capacity_rows < 0 || bad_range(ctx, p_begin, p_end)) return ULTRAEP_EINVAL;
   if (accumulate != 0 && accumulate != 1) return ULTRAEP_EINVAL;
   if (N % 8 != 0 || K % 8 != 0 || N > kMaxWidth || K > kMaxWidth || capacity_rows >= kMaxRows ||
-      !aligned(plan, 4) || !aligned(dyt, 16) || !aligned(xt, 16) || !aligned(dyt_scale, 8) ||
-      !aligned(xt_scale, 8) || !aligned(grads, 8))
+      !aligned(plan, 4) || !aligned(dyt, 16) || !aligned(xt, 16) || !aligned(grads, 8) ||
+      static_cast<int64_t>(p_end - p_begin) * ((N + 255) / 256) * ((K + 255) / 256) > kMaxTiles)
     return ULTRAEP_EUNSUPPORTED;
   return from_hip(ultraep::launch_expert_wgrad(segment(ctx, plan, p_begin), p_end - p_begin, dyt, dyt_scale, N,
                                                xt, xt_scale, K, capacity_rows, grads, accumulate != 0,

@@ -29,6 +29,7 @@ constexpr int kGradBlocks = ULTRAEP_GRAD_WORKSPACE_BYTES / 8;  // partial sums
 
 // Vectors at any alignment of their elements, in global memory (addresses from
 // a table would otherwise be loaded as generic ones).
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
 typedef __attribute__((address_space(1))) u32x4_any global_vec;
 typedef __attribute__((address_space(1))) uint16_t global_u16;
@@ -42,53 +43,55 @@ __device__ __forceinline__ void store_vec(uintptr_t p, const u32x4& v) {
 }
 
 // The workgroup's walk over the chunks: first[t] is the number of chunks before
-// tensor t, `total` the number of all.
+// tensor t (2^31 chunks would be 32 TiB), `total` the number of all.
 struct Walk {
   const void* const* tensors;
   const int64_t* numels;
   int32_t n;
-  const int64_t* first;
-  int64_t total;
+  const int32_t* first;
+  int32_t total;
 };
 
 struct Chunk {
   uintptr_t p;     // its first element
-  int64_t len;     // elements
   int64_t at;      // elements of the tensor before it
+  int32_t len;     // elements
   int32_t tensor;
 };
 
-// Chunk c < total, at or behind `from`'s tensor.
-__device__ __forceinline__ Chunk chunk_at(const Walk& w, int64_t c, int32_t from, int32_t per_chunk, int32_t size) {
+// Chunk c < total; its tensor is `from` or a later one.
+__device__ __forceinline__ Chunk chunk_at(const Walk& w, int32_t c, int32_t from, int32_t per_chunk, int32_t size) {
+  int32_t lo = from, step = 1;  // doubling steps, then halving ones
+  while (lo + step < w.n && w.first[lo + step] <= c) {
+    lo += step;
+    step *= 2;
+  }
+  for (; step > 0; step >>= 1)
+    if (lo + step < w.n && w.first[lo + step] <= c) lo += step;
   Chunk x;
-  x.tensor = from;
-  while (x.tensor + 1 < w.n && w.first[x.tensor + 1] <= c) ++x.tensor;
-  x.at = (c - w.first[x.tensor]) * per_chunk;
-  x.len = min(w.numels[x.tensor] - x.at, static_cast<int64_t>(per_chunk));
-  x.p = reinterpret_cast<uintptr_t>(w.tensors[x.tensor]) + x.at * size;
+  x.tensor = lo;
+  x.at = static_cast<int64_t>(c - w.first[lo]) * per_chunk;
+  x.len = static_cast<int32_t>(min(w.numels[lo] - x.at, static_cast<int64_t>(per_chunk)));
+  x.p = reinterpret_cast<uintptr_t>(w.tensors[lo]) + x.at * size;
   return x;
 }
 
-__device__ Walk grad_walk(const void* const* tensors, const int64_t* numels, int32_t n, int32_t per_chunk, int64_t* first) {
-  __shared__ int64_t s_wave[kGradThreads / 64];
+__device__ Walk grad_walk(const void* const* tensors, const int64_t* numels, int32_t n, int32_t per_chunk, int32_t* first) {
+  __shared__ int32_t s_wave[kGradThreads / 64];
   const int tid = threadIdx.x, lane = lane_id(), wv = tid >> 6;
   const int32_t each = (n + kGradThreads - 1) / kGradThreads;
   const int32_t t0 = min(tid * each, n), t1 = min(t0 + each, n);
-  int64_t sum = 0;
+  int32_t sum = 0;
   for (int32_t t = t0; t < t1; ++t) {
+    const int64_t m = numels[t];
+    const bool some = tensors[t] != nullptr;  // both loads at once
     first[t] = sum;
-    const int64_t m = tensors[t] == nullptr ? 0 : numels[t];
-    sum += m > 0 ? (m + per_chunk - 1) / per_chunk : 0;
+    sum += some && m > 0 ? static_cast<int32_t>((m + per_chunk - 1) / per_chunk) : 0;
   }
-  int64_t scan = sum;  // inclusive over the wave
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int64_t y = __shfl_up(scan, d);
-    if (lane >= d) scan += y;
-  }
-  if (lane == 63) s_wave[wv] = scan;
+  const int32_t upto = wave_inclusive_scan(sum);
+  if (lane == 63) s_wave[wv] = upto;
   __syncthreads();
-  int64_t before = scan - sum, total = 0;
+  int32_t before = upto - sum, total = 0;
 #pragma unroll
   for (int i = 0; i < kGradThreads / 64; ++i) {
     if (i < wv) before += s_wave[i];
@@ -122,10 +125,25 @@ __device__ __forceinline__ double squares(const u32x4& v) {
   return s;
 }
 
+template <int CTRL>
+__device__ __forceinline__ double dpp_f64(double v) {
+  const u32x2 x = __builtin_bit_cast(u32x2, v);
+  const u32x2 y = {dpp<CTRL>(x[0]), dpp<CTRL>(x[1])};
+  return __builtin_bit_cast(double, y);
+}
+
+__device__ __forceinline__ double readlane_f64(double v, int l) {
+  const u32x2 x = __builtin_bit_cast(u32x2, v);
+  const u32x2 y = {readlane(x[0], l), readlane(x[1], l)};
+  return __builtin_bit_cast(double, y);
+}
+
 __device__ __forceinline__ double wave_sum_f64(double x) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) x += __shfl_xor(x, d);
-  return x;
+  x += dpp_f64<0xB1>(x);
+  x += dpp_f64<0x4E>(x);
+  x += dpp_f64<0x141>(x);
+  x += dpp_f64<0x140>(x);
+  return ((readlane_f64(x, 0) + readlane_f64(x, 16)) + readlane_f64(x, 32)) + readlane_f64(x, 48);
 }
 
 // Sum over the workgroup, in thread 0.
@@ -141,13 +159,14 @@ template <bool BF16>
 __global__ __launch_bounds__(kGradThreads) void grad_sumsq_kernel(const void* const* __restrict__ tensors,
                                                                   const int64_t* __restrict__ numels, int32_t n,
                                                                   double* __restrict__ partial) {
-  extern __shared__ int64_t s_first[];
+  extern __shared__ int32_t s_first[];
   constexpr int kSize = BF16 ? 2 : 4, kVec = 16 / kSize, kChunk = kGradBytes / kSize;
   const Walk w = grad_walk(tensors, numels, n, kChunk, s_first);
   double acc = 0.0;
   Chunk x, next;
-  if (blockIdx.x < w.total) next = chunk_at(w, blockIdx.x, 0, kChunk, kSize);
-  for (int64_t c = blockIdx.x; c < w.total; c += gridDim.x) {
+  const int32_t blocks = static_cast<int32_t>(gridDim.x);
+  if (static_cast<int32_t>(blockIdx.x) < w.total) next = chunk_at(w, static_cast<int32_t>(blockIdx.x), 0, kChunk, kSize);
+  for (int32_t c = static_cast<int32_t>(blockIdx.x); c < w.total; c += blocks) {
     x = next;
     u32x4 v[kGradVecs];
 #pragma unroll
@@ -156,12 +175,12 @@ __global__ __launch_bounds__(kGradThreads) void grad_sumsq_kernel(const void* co
       v[u] = u32x4{0, 0, 0, 0};
       if (i + kVec <= x.len) v[u] = load_vec(x.p + i * kSize);
     }
-    if (c + gridDim.x < w.total) next = chunk_at(w, c + gridDim.x, x.tensor, kChunk, kSize);
+    if (c + blocks < w.total) next = chunk_at(w, c + blocks, x.tensor, kChunk, kSize);
 #pragma unroll
     for (int u = 0; u < kGradVecs; ++u) acc += squares<BF16>(v[u]);
-    const int rest = static_cast<int>(x.len % kVec);  // values behind the last whole vector
+    const int rest = x.len % kVec;  // values behind the last whole vector
     if (static_cast<int>(threadIdx.x) < rest) {
-      const int64_t i = x.len - rest + threadIdx.x;
+      const int i = x.len - rest + static_cast<int>(threadIdx.x);
       acc += square(BF16 ? bf16_lo(reinterpret_cast<const global_u16*>(x.p)[i]) : reinterpret_cast<const global_f32*>(x.p)[i]);
     }
   }
@@ -182,7 +201,7 @@ __global__ __launch_bounds__(kGradThreads) void grad_clip_kernel(const void* con
                                                                  const int64_t* __restrict__ numels, int32_t n,
                                                                  const double* __restrict__ sumsq, double max_norm,
                                                                  float* __restrict__ norm_out, void* const* __restrict__ out) {
-  extern __shared__ int64_t s_first[];
+  extern __shared__ int32_t s_first[];
   constexpr int kSize = BF16 ? 2 : 4, kVec = 16 / kSize, kChunk = kGradBytes / kSize;
   const double norm = sqrt(*sumsq), ratio = max_norm / (norm + 1e-6);
   const double coef = ratio >= 1.0 ? 1.0 : ratio;  // NaN stays NaN; fp64, since a huge norm's factor is below fp32's range
@@ -190,8 +209,9 @@ __global__ __launch_bounds__(kGradThreads) void grad_clip_kernel(const void* con
   if (coef == 1.0 && out == nullptr) return;
   const Walk w = grad_walk(tensors, numels, n, kChunk, s_first);
   Chunk x, next;
-  if (blockIdx.x < w.total) next = chunk_at(w, blockIdx.x, 0, kChunk, kSize);
-  for (int64_t c = blockIdx.x; c < w.total; c += gridDim.x) {
+  const int32_t blocks = static_cast<int32_t>(gridDim.x);
+  if (static_cast<int32_t>(blockIdx.x) < w.total) next = chunk_at(w, static_cast<int32_t>(blockIdx.x), 0, kChunk, kSize);
+  for (int32_t c = static_cast<int32_t>(blockIdx.x); c < w.total; c += blocks) {
     x = next;
     u32x4 v[kGradVecs];
 #pragma unroll
@@ -201,7 +221,7 @@ __global__ __launch_bounds__(kGradThreads) void grad_clip_kernel(const void* con
     }
     const uintptr_t to = out == nullptr ? 0 : reinterpret_cast<uintptr_t>(out[x.tensor]);
     const uintptr_t d = to == 0 ? x.p : to + x.at * kSize;
-    if (c + gridDim.x < w.total) next = chunk_at(w, c + gridDim.x, x.tensor, kChunk, kSize);
+    if (c + blocks < w.total) next = chunk_at(w, c + blocks, x.tensor, kChunk, kSize);
     if (coef == 1.0 && d == x.p) continue;
 #pragma unroll
     for (int u = 0; u < kGradVecs; ++u) {
@@ -214,9 +234,9 @@ __global__ __launch_bounds__(kGradThreads) void grad_clip_kernel(const void* con
                     : bits_of(scaled(coef, f32_of(v[u][j])));
       store_vec(d + i * kSize, y);
     }
-    const int rest = static_cast<int>(x.len % kVec);
+    const int rest = x.len % kVec;
     if (static_cast<int>(threadIdx.x) < rest) {
-      const int64_t i = x.len - rest + threadIdx.x;
+      const int i = x.len - rest + static_cast<int>(threadIdx.x);
       if (BF16)
         reinterpret_cast<global_u16*>(d)[i] =
             static_cast<uint16_t>(pack_bf16(scaled(coef, bf16_lo(reinterpret_cast<const global_u16*>(x.p)[i])), 0.f));
@@ -233,9 +253,9 @@ hipError_t launch_grad_sumsq(const void* const* tensors, const int64_t* numels, 
   const int32_t grid = n > 0 ? kGradBlocks : 0;
   if (grid > 0) {
     if (bf16)
-      hipLaunchKernelGGL(grad_sumsq_kernel<true>, dim3(grid), dim3(kGradThreads), n * sizeof(int64_t), st, tensors, numels, n, partial);
+      hipLaunchKernelGGL(grad_sumsq_kernel<true>, dim3(grid), dim3(kGradThreads), n * sizeof(int32_t), st, tensors, numels, n, partial);
     else
-      hipLaunchKernelGGL(grad_sumsq_kernel<false>, dim3(grid), dim3(kGradThreads), n * sizeof(int64_t), st, tensors, numels, n, partial);
+      hipLaunchKernelGGL(grad_sumsq_kernel<false>, dim3(grid), dim3(kGradThreads), n * sizeof(int32_t), st, tensors, numels, n, partial);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -248,9 +268,9 @@ hipError_t launch_grad_clip(const void* const* tensors, const int64_t* numels, i
                             hipStream_t st) {
   const int32_t grid = n > 0 ? kGradBlocks : 1;
   if (bf16)
-    hipLaunchKernelGGL(grad_clip_kernel<true>, dim3(grid), dim3(kGradThreads), n * sizeof(int64_t), st, tensors, numels, n, sumsq, max_norm, norm, out);
+    hipLaunchKernelGGL(grad_clip_kernel<true>, dim3(grid), dim3(kGradThreads), n * sizeof(int32_t), st, tensors, numels, n, sumsq, max_norm, norm, out);
   else
-    hipLaunchKernelGGL(grad_clip_kernel<false>, dim3(grid), dim3(kGradThreads), n * sizeof(int64_t), st, tensors, numels, n, sumsq, max_norm, norm, out);
+    hipLaunchKernelGGL(grad_clip_kernel<false>, dim3(grid), dim3(kGradThreads), n * sizeof(int32_t), st, tensors, numels, n, sumsq, max_norm, norm, out);
   return hipGetLastError();
 }
 

@@ -88,8 +88,8 @@ def test_expert_wgrad_refusals(ctx):
     for bad in (dict(c=None), dict(plan=None), dict(dy=None), dict(dys=None), dict(x=None), dict(xs=None), dict(g=None),
                 dict(N=0), dict(K=0), dict(cap=-1), dict(p1=13), dict(p0=4), dict(acc=2)):
         assert call(**bad) == -1, bad
-    for bad in (dict(N=12), dict(K=12), dict(dy=F + 8), dict(dys=F + 4), dict(x=F + 8), dict(xs=F + 4), dict(g=F + 4),
-                dict(cap=1 << 31), dict(K=(1 << 20) + 8)):
+    for bad in (dict(N=12), dict(K=12), dict(dy=F + 8), dict(x=F + 8), dict(g=F + 4),
+                dict(cap=1 << 31), dict(K=(1 << 20) + 8), dict(N=1 << 20, K=1 << 20)):
         assert call(**bad) == -2, bad
     assert call(p0=2, p1=2) == 0
 
