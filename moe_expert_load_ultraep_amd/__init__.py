@@ -300,16 +300,16 @@ def pointer_table(tensors, device="cuda"):
     return torch.tensor([0 if t is None else t.data_ptr() for t in tensors], dtype=torch.int64).to(device)
 
 
-_F8 = _F16 = _I64 = _I32 = _device = None
+_BYTES = _HALVES = _LONGS = _INTS = _device = None
 
 
 def _types():
     """The types a call's buffers may have, and the current device's index, found once torch is in use."""
-    global _F8, _F16, _I64, _I32, _device
+    global _BYTES, _HALVES, _LONGS, _INTS, _device
     import torch
-    _F8 = (torch.uint8, torch.float8_e4m3fn)
-    _F16 = (torch.bfloat16, torch.int16, torch.uint16)
-    _I64, _I32 = (torch.int64,), (torch.int32,)
+    _BYTES = (torch.uint8, torch.float8_e4m3fn)
+    _HALVES = (torch.bfloat16, torch.int16, torch.uint16)
+    _LONGS, _INTS = (torch.int64,), (torch.int32,)
     _device = lambda: torch.cuda.current_device() if torch.cuda.is_initialized() else None  # noqa: E731
 
 
@@ -323,6 +323,8 @@ def _here():
 def _is(t, dev, dtypes, *shape) -> bool:
     """A contiguous tensor of the current device with one of the types and this shape; the first extent may be
     None (any)."""
+    if t is None:
+        return False
     s = t.shape
     return (t.get_device() == dev and t.dtype in dtypes and t.is_contiguous()
             and (s == shape if shape[0] is not None else len(s) == len(shape) and s[1:] == shape[1:]))
@@ -330,7 +332,8 @@ def _is(t, dev, dtypes, *shape) -> bool:
 
 def _is_plan(ctx, plan, dev) -> bool:
     """One plan record of the context."""
-    return plan.get_device() == dev and plan.is_contiguous() and plan.numel() * plan.element_size() >= ctx.plan_bytes
+    return (plan is not None and plan.get_device() == dev and plan.is_contiguous()
+            and plan.numel() * plan.element_size() >= ctx.plan_bytes)
 
 
 def _need(fn: str, ok: bool) -> None:
@@ -348,18 +351,18 @@ def ultraep_permute_quant(ctx: Context, plan, inv, k: int, hidden, p_begin: int,
     fn = "ultraep_permute_quant"
     dev = _here()
     _need(fn, (q is None) == (q_scale is None) and (qt is None) == (qt_scale is None) and not (q is None and qt is None)
-          and hidden.dim() == 2 and (rows is not None or q is not None))
+          and hidden is not None and hidden.dim() == 2 and (rows is not None or q is not None))
     H = hidden.shape[1]
     if rows is None:
         rows = q.shape[0]
     blocks = 0
-    _need(fn, _is_plan(ctx, plan, dev) and _is(hidden, dev, _F16, None, H) and (inv is None or _is(inv, dev, _I32, None)))
+    _need(fn, _is_plan(ctx, plan, dev) and _is(hidden, dev, _HALVES, None, H) and (inv is None or _is(inv, dev, _INTS, None)))
     if q is not None:
-        _need(fn, _is(q, dev, _F8, None, quant_pitch(H)) and _is(q_scale, dev, _F8, q.shape[0], quant_scale_pitch(H))
+        _need(fn, _is(q, dev, _BYTES, None, quant_pitch(H)) and _is(q_scale, dev, _BYTES, q.shape[0], quant_scale_pitch(H))
               and rows <= q.shape[0])
     if qt is not None:
         blocks = qt.shape[0]
-        _need(fn, _is(qt, dev, _F8, None, H, QUANT_BLOCK) and _is(qt_scale, dev, _F8, blocks, H))
+        _need(fn, _is(qt, dev, _BYTES, None, H, QUANT_BLOCK) and _is(qt_scale, dev, _BYTES, blocks, H))
     st = lib().ultraep_permute_quant(ctx.handle, _ptr(plan), _ptr(inv), k, _ptr(hidden), hidden.shape[0], H, p_begin,
                                      p_end, _ptr(q), _ptr(q_scale), _ptr(qt), _ptr(qt_scale), rows, blocks,
                                      _stream(stream))
@@ -373,11 +376,11 @@ def ultraep_weight_quant(ctx: Context, weights, n: int, N: int, K: int, q=None, 
     fn = "ultraep_weight_quant"
     dev = _here()
     _need(fn, (q is None) == (q_scale is None) and (qt is None) == (qt_scale is None)
-          and _is(weights, dev, _I64, None) and weights.shape[0] >= n)
+          and _is(weights, dev, _LONGS, None) and weights.shape[0] >= n)
     for a, b, x, xs in ((N, K, q, q_scale), (K, N, qt, qt_scale)):
         if x is not None:
-            _need(fn, _is(x, dev, _F8, None, a, quant_pitch(b))
-                  and _is(xs, dev, _F8, None, quant_pitch(a) // QUANT_BLOCK, quant_scale_pitch(b))
+            _need(fn, _is(x, dev, _BYTES, None, a, quant_pitch(b))
+                  and _is(xs, dev, _BYTES, None, quant_pitch(a) // QUANT_BLOCK, quant_scale_pitch(b))
                   and x.shape[0] >= n and xs.shape[0] >= n)
     st = lib().ultraep_weight_quant(ctx.handle, _ptr(weights), n, N, K, _ptr(q), _ptr(q_scale), _ptr(qt),
                                     _ptr(qt_scale), _stream(stream))
@@ -391,9 +394,9 @@ def ultraep_expert_gemm(ctx: Context, plan, q, q_scale, K: int, w, w_scale, N: i
     w, w_scale: int64 device tensors [p_end - p_begin] of pointers to the quantised weights and scales."""
     fn = "ultraep_expert_gemm"
     dev = _here()
-    _need(fn, _is_plan(ctx, plan, dev) and _is(q, dev, _F8, None, quant_pitch(K)) and _is(q_scale, dev, _F8, q.shape[0], quant_scale_pitch(K))
-          and _is(w, dev, _I64, None) and _is(w_scale, dev, _I64, None) and w.shape[0] >= p_end - p_begin
-          and w_scale.shape[0] >= p_end - p_begin and _is(out, dev, _F16, None, N))
+    _need(fn, _is_plan(ctx, plan, dev) and _is(q, dev, _BYTES, None, quant_pitch(K)) and _is(q_scale, dev, _BYTES, q.shape[0], quant_scale_pitch(K))
+          and _is(w, dev, _LONGS, None) and _is(w_scale, dev, _LONGS, None) and w.shape[0] >= p_end - p_begin
+          and w_scale.shape[0] >= p_end - p_begin and _is(out, dev, _HALVES, None, N))
     st = lib().ultraep_expert_gemm(ctx.handle, _ptr(plan), _ptr(q), _ptr(q_scale), K, _ptr(w), _ptr(w_scale), N,
                                    p_begin, p_end, _ptr(out), min(out.shape[0], q.shape[0]), _stream(stream))
     _check(fn, st)
@@ -404,9 +407,9 @@ def ultraep_expert_wgrad(ctx: Context, plan, dyt, dyt_scale, N: int, xt, xt_scal
     """grads: int64 device tensor [p_end - p_begin] of pointers to fp32 [N, K]; rows: the segment's capacity."""
     fn = "ultraep_expert_wgrad"
     dev = _here()
-    _need(fn, rows >= 0 and _is_plan(ctx, plan, dev) and _is(dyt, dev, _F8, None, N, QUANT_BLOCK) and _is(dyt_scale, dev, _F8, dyt.shape[0], N)
-          and _is(xt, dev, _F8, None, K, QUANT_BLOCK) and _is(xt_scale, dev, _F8, xt.shape[0], K)
-          and min(dyt.shape[0], xt.shape[0]) >= quant_blocks(rows, p_end - p_begin) and _is(grads, dev, _I64, None)
+    _need(fn, rows >= 0 and _is_plan(ctx, plan, dev) and _is(dyt, dev, _BYTES, None, N, QUANT_BLOCK) and _is(dyt_scale, dev, _BYTES, dyt.shape[0], N)
+          and _is(xt, dev, _BYTES, None, K, QUANT_BLOCK) and _is(xt_scale, dev, _BYTES, xt.shape[0], K)
+          and min(dyt.shape[0], xt.shape[0]) >= quant_blocks(rows, p_end - p_begin) and _is(grads, dev, _LONGS, None)
           and grads.shape[0] >= p_end - p_begin)
     st = lib().ultraep_expert_wgrad(ctx.handle, _ptr(plan), _ptr(dyt), _ptr(dyt_scale), N, _ptr(xt), _ptr(xt_scale), K,
                                     p_begin, p_end, rows, _ptr(grads), int(accumulate), _stream(stream))
@@ -417,7 +420,7 @@ def _grad_checks(fn: str, tensors, numels, n: int, dtype, sumsq) -> tuple:
     """(current device, dtype code) of a call over gradient tensors."""
     import torch
     dev = _here()
-    _need(fn, _is(tensors, dev, _I64, None) and _is(numels, dev, _I64, None) and tensors.shape[0] >= n
+    _need(fn, _is(tensors, dev, _LONGS, None) and _is(numels, dev, _LONGS, None) and tensors.shape[0] >= n
           and numels.shape[0] >= n and _is(sumsq, dev, (torch.float64,), 1)
           and (dtype is torch.float32 or dtype is torch.bfloat16))
     return dev, int(dtype is torch.bfloat16)
@@ -429,7 +432,7 @@ def ultraep_grad_sumsq(ctx: Context, tensors, numels, n: int, dtype, sumsq, work
     workspace: GRAD_WORKSPACE_BYTES)."""
     fn = "ultraep_grad_sumsq"
     dev, code = _grad_checks(fn, tensors, numels, n, dtype, sumsq)
-    _need(fn, workspace.get_device() == dev and workspace.is_contiguous())
+    _need(fn, workspace is not None and workspace.get_device() == dev and workspace.is_contiguous())
     st = lib().ultraep_grad_sumsq(ctx.handle, _ptr(tensors), _ptr(numels), n, code, _ptr(sumsq), int(accumulate),
                                   _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
     _check(fn, st)

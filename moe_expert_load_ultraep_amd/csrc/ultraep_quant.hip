@@ -127,15 +127,16 @@ __global__ __launch_bounds__(kQuantThreads) void quant_cols_kernel(
     u32x4 x[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = u32x4{0, 0, 0, 0};
-    if (in.hidden_rows > 0)
+    if (in.hidden_rows > 0) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = 8 * g + i;
-      const int32_t tok = static_cast<int32_t>(source_row(in, seg0, row0 + min(r, live - 1)));
-      x[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(in.hidden + static_cast<int64_t>(max(tok, 0)) * H + hc));
-      const uint32_t keep = r < live && tok >= 0 && h0 < H ? 0xFFFFFFFFu : 0u;
+      for (int i = 0; i < 8; ++i) {
+        const int r = 8 * g + i;
+        const int32_t tok = static_cast<int32_t>(source_row(in, seg0, row0 + min(r, live - 1)));
+        x[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(in.hidden + static_cast<int64_t>(max(tok, 0)) * H + hc));
+        const uint32_t keep = r < live && tok >= 0 && h0 < H ? 0xFFFFFFFFu : 0u;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[i][j] &= keep;
+        for (int j = 0; j < 4; ++j) x[i][j] &= keep;
+      }
     }
     if (ROWS) {
       const __amdgpu_buffer_rsrc_t to_q = row_rsrc(q + row0 * Hp, static_cast<uint32_t>(live) * static_cast<uint32_t>(Hp));

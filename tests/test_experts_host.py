@@ -129,3 +129,17 @@ def test_binding_refuses_host_tensors_and_wrong_types(ctx):
         with pytest.raises(U.UltraEPError) as ei:
             f()
         assert ei.value.status == -1
+
+
+def test_binding_refuses_missing_buffers(ctx):
+    table = torch.zeros(3, dtype=torch.int64)
+    for f in (lambda: U.ultraep_permute_quant(ctx, table, None, 1, None, 0, 3, table, table),
+              lambda: U.ultraep_permute_quant(ctx, None, None, 1, torch.zeros(4, 64), 0, 3, table, table),
+              lambda: U.ultraep_weight_quant(ctx, None, 3, 64, 64, table, table),
+              lambda: U.ultraep_expert_gemm(ctx, None, table, table, 64, table, table, 64, 0, 3, table),
+              lambda: U.ultraep_expert_wgrad(ctx, None, table, table, 64, table, table, 64, 0, 3, 4, table),
+              lambda: U.ultraep_grad_sumsq(ctx, None, table, 3, torch.float32, table, table),
+              lambda: U.ultraep_grad_clip(ctx, None, table, 3, torch.float32, table, 1.0)):
+        with pytest.raises(U.UltraEPError) as ei:
+            f()
+        assert ei.value.status == -1
