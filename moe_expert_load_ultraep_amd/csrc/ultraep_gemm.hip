@@ -74,7 +74,7 @@ struct BigOperand {
 // into 16 where it is fp32.
 //
 // Half H of an operand's block is what the two waves along it read as fragments
-// 4H..4H+3, 64 rows each: row s of the half is this row of the tile. 
+// 4H..4H+3, 64 rows each: row s of the half is this row of the tile.
 template <bool PAIRS, int H>
 __device__ __forceinline__ int half_row(int s) {
   return PAIRS ? 128 * (s >> 6) + 64 * H + (s & 63) : 128 * H + s;
@@ -311,7 +311,7 @@ __device__ __forceinline__ bool usable(const uint8_t* w, const uint8_t* ws) {
 // Bound by the matrix units' rate at the clock they leave (about 2.0 GHz), and
 // next to that by the loads into LDS: alone, the products of a block of a full
 // tile take 1.0-1.3 us, its 64 KiB of loads 1.5 us, together 1.55 us.  Larger
-// tiles do not fit the registers.  32768 rows by 6 experts of 4096 x 7168: 740-780
+// tiles do not fit the registers.  32768 rows by 6 experts of 4096 x 7168: 730-780
 // us, 2.5-2.6 PFLOP/s; 8192 x 8192 x 8192: 430 us, 2.56 PFLOP/s (a library's plain 8-bit
 // product reaches 2.71-2.78 there).  Measured and not kept: one workgroup a CU that
 // walks the tiles and loads the next one's blocks before it stores (829 us: the
@@ -443,12 +443,12 @@ __device__ __forceinline__ i32x8 thin_fragment(const uint8_t* row) {
 
 // 32 weight rows by 16 rows.  The four waves split the blocks of 128
 // (wave v takes v, v + 4, ...), every weight byte goes from memory to the
-// registers of the one wave that uses it, DEPTH blocks ahead, and the waves'
-// sums meet in LDS and are added in wave order.  Bound by HBM: 41 rows by 6
-// experts of 4096 x 7168 (177 MB) take 34 us, 5.2 TB/s, the rate of a large copy.
-// Two or eight waves a tile take 38 us with 64 columns, four 36; 128 columns a
-// tile 43; loads two blocks ahead are slower (fewer waves fit), as are
-// non-temporal loads (46 us).
+// registers of the one wave that uses it, the next block's while this one is
+// multiplied, and the waves' sums meet in LDS and are added in wave order.
+// Bound by HBM: 41 rows by 6 experts of 4096 x 7168 (177 MB) take 34-37 us, 4.8-5.2
+// TB/s, the rate of a large copy.  With 64 columns a tile 36-38 us with four
+// waves, 38 with two or eight; 128 columns 43; loads two blocks ahead are slower
+// (fewer waves fit), as are non-temporal loads (46 us).
 __global__ __launch_bounds__(kThinThreads) void expert_gemm_thin_kernel(GemmArgs g, int32_t ntile) {
   constexpr int FN = kThinCols / 16;
   __shared__ __align__(16) float s_sum[kThinWaves][kThinRows][kThinCols + 4];
@@ -642,11 +642,11 @@ __device__ __forceinline__ int32_t expert_of_rank(const int32_t* off, int32_t ne
 // grads[p][n][k]: A is x (a lane holds four consecutive k of a row n), B is dy.
 //
 // Bound by the bf16 products at the clock they leave.  32768 rows, 6 experts of
-// 4096 x 7168: 1352 us, 1.42 PFLOP/s (a library's plain bf16 product reaches 1.24
-// at 8192 x 8192 x 8192); without the loads 1200 us.  With the tiles dealt to the
-// XCDs in one walk over all experts it took 2260 us: an XCD got whole experts.
-// Widening spread over all eight products of a step instead of the first four:
-// 1404 us.
+// 4096 x 7168: 1256-1296 us, 1.5 PFLOP/s (a library's plain bf16 product reaches
+// 1.24 at 8192 x 8192 x 8192).  Before the stores covered whole lines it took 1352
+// us, and against that: 1200 without the loads (a bound, not a result), 2260 with
+// the tiles dealt to the XCDs in one walk over all experts (an XCD got whole
+// experts), 1404 with the widening spread over all eight products of a step.
 __global__ __launch_bounds__(kMmThreads, 1) void expert_wgrad_big_kernel(
     const int32_t* off, int32_t ne, const uint8_t* dyt, const uint8_t* dyt_scale, int32_t N, const uint8_t* xt,
     const uint8_t* xt_scale, int32_t K, int64_t cap, float* const* grads, bool accumulate, int32_t ntile,
@@ -763,11 +763,17 @@ hipError_t launch_expert_gemm(const int32_t* off, int32_t ne, const uint8_t* q, 
   if (ne == 0 || cap == 0) return hipSuccess;
   const GemmArgs g{off, ne, q, q_scale, K, w, w_scale, N, out, cap};
   const int32_t nbig = ceil_div(N, kBigTile);
-  // Few rows.  With 6 experts of 4096 x 7168 (96 big tiles, too few to draw all
-  // of the memory's rate) thin tiles take 21 / 30 / 32 / 40 / 58 us at 1 / 4 / 8 /
-  // 12 / 16 rows an expert, big ones 46 / 46 / 49 / 50 / 54; with 24 experts of
-  // 2048 x 5120 (192 big tiles) 50 / 57 us at 4 / 8 rows, big ones 49 / 50.
-  if (cap <= 4 * static_cast<int64_t>(ne) || (cap <= 12 * static_cast<int64_t>(ne) && static_cast<int64_t>(ne) * nbig < 128)) {
+  // Few rows.  Thin tiles take each row tile's weights from memory at 5.2 TB/s,
+  // cap / 16 + ne / 2 or so row tiles; big ones 0.8 us a block of 128 of K and
+  // more the more of them share the memory, whatever the rows.  Both grow with
+  // K alike, which leaves a bound on rows and N; and up to four rows an expert
+  // nearly every thin tile is its expert's only one.  Thin / big, us: 6 experts of
+  // 4096 x 7168 at 1, 4, 8, 12, 16, 24 rows an expert 23/48, 34/52, 38/55, 46/55,
+  // 55/57, 66/58; 24 of 2048 x 5120 at 1, 4, 8: 32/45, 50/51, 61/52; 32 of 7168 x
+  // 2048 at 1, 4, 8: 59/66, 86/87, 108/91; 4 of 1536 x 5120 at 16, 32, 50, 70: 16/31,
+  // 19/32, 27/32, 34/33; one of 4096 x 7168 at 64, 96, 128: 24/41, 36/41, 46/42; 8 of
+  // 1024 x 1024 at 32, 55: 9.3/11.2, 11.7/11.4; 16 of 512 x 2048 at 32, 50: 14/17, 18/17.
+  if (cap <= 4 * static_cast<int64_t>(ne) || (cap + 4 * static_cast<int64_t>(ne)) * N <= 420000) {
     const int32_t ntile = ceil_div(N, kThinCols);
     const int64_t tiles = (cap / kThinRows + ne) * ntile;
     hipLaunchKernelGGL(expert_gemm_thin_kernel, dim3(mm_grid(tiles)), dim3(kThinThreads), 0, st, g, ntile);

@@ -6,7 +6,7 @@
 // chunk counts into LDS once and takes every gridDim-th chunk, so tensors of any
 // sizes spread evenly, neighbouring chunks are read at one time, and the order of
 // every sum depends on the sizes alone.  Bound by HBM: 4e8 fp32 elements, read
-// twice and written once (4.8 GB), take 915 us, 5.2 TB/s, the rate of a large
+// twice and written once (4.8 GB), take 905-915 us, 5.3 TB/s, the rate of a large
 // copy.  One contiguous share a workgroup took 977 us, ordinary instead of
 // non-temporal accesses 930, two vectors in flight 934, eight 1002 (fewer waves
 // fit), half as many workgroups 967.  The squares are added in fp64, whose cost

@@ -264,6 +264,41 @@ def test_expert_gemm_tiles_of_256_rows(loads, N, K):
     assert np.array_equal(np.where(got == 0x8000, 0, got), np.where(want == 0x8000, 0, want))
 
 
+@pytest.mark.parametrize("loads", [[300, 0, 40, 3, 0, 0, 17, 500, 64, 0], [127, 1, 0, 129, 255, 257], [256, 128, 128]],
+                         ids=lambda v: f"{len(v)}x{sum(v)}")
+@pytest.mark.parametrize("N,K", [(1800, 8), (1544, 264), (1288, 1000)])
+def test_expert_gemm_tiles_of_128_rows(loads, N, K):
+    """Too many rows for the thin tiles and too few for the full height."""
+    say(f"expert_gemm 128-row tiles loads={loads} N={N} K={K}")
+    rng = np.random.default_rng([N, K, sum(loads)])
+    seg, q, qs, w, ws = operands(rng, loads, N, K, whole=True)
+    got = run_gemm(seg, q, qs, w, ws, N, K)
+    want, _ = to_bf16(X.expert_gemm(*gemm_values(seg, q, qs, w, ws), seg.off) + 0.0)
+    zero = lambda a: np.where(a == 0x8000, 0, a)  # noqa: E731
+    assert np.array_equal(zero(got[:seg.rows]), zero(want))
+    assert (got[seg.rows:] == 0x7FC1).all()
+
+
+@pytest.mark.parametrize("loads,N", [([200, 33, 300], 1544), ([700, 100], 4104)])
+def test_expert_gemm_large_tiles_real_values_missing_weights_and_nan(loads, N):
+    rng = np.random.default_rng(N)
+    K = 520
+    seg, q, qs, w, ws = operands(rng, loads, N, K, whole=False)
+    q[150, 500] = 0x7F
+    got = run_gemm(seg, q, qs, w, ws, N, K, cap=seg.rows - 10, holes=(1,))
+    q[150, 500] = 0
+    x, wv = gemm_values(seg, q, qs, w, ws)
+    want = X.expert_gemm(x, wv, seg.off)
+    mag = X.expert_gemm(np.abs(x), [np.abs(v) for v in wv], seg.off)
+    val = (got.astype(np.uint32) << 16).view(np.float32).astype(np.float64)
+    slack = (GROUP_CUT + K * F32_ADD) * mag
+    ok = np.abs(val - want[:len(val)]) <= (slack + BF16_STEP * (np.abs(want) + slack))[:len(val)]
+    ok[150] = np.isnan(val[150])
+    a, b = loads[0], loads[0] + loads[1]
+    ok[a:b] = got[a:b] == 0x7FC1
+    assert ok.all()
+
+
 def test_expert_gemm_skips_missing_weights_and_cuts_at_the_capacity():
     rng = np.random.default_rng(8)
     seg, q, qs, w, ws = operands(rng, [40, 300, 5, 60], 264, 136, whole=True)
