@@ -55,6 +55,7 @@ typedef __attribute__((address_space(3))) uint8_t lds_u8;
 typedef __attribute__((address_space(1))) int global_int;
 
 constexpr int kBigTile = 256;        // rows of either operand
+constexpr int kComputeUnits = 256;
 constexpr int kHalfBytes = 128 * 128;  // half of an operand's block of 128, in LDS
 
 // One operand of a tile: row r of block b at base + min(r, last) * row_pitch +
@@ -312,12 +313,14 @@ __device__ __forceinline__ bool usable(const uint8_t* w, const uint8_t* ws) {
 // next to that by the loads into LDS: alone, the products of a block of a full
 // tile take 1.0-1.3 us, its 64 KiB of loads 1.5 us, together 1.55 us.  Larger
 // tiles do not fit the registers.  32768 rows by 6 experts of 4096 x 7168: 730-780
-// us, 2.5-2.6 PFLOP/s; 8192 x 8192 x 8192: 430 us, 2.56 PFLOP/s (a library's plain 8-bit
-// product reaches 2.71-2.78 there).  Measured and not kept: one workgroup a CU that
-// walks the tiles and loads the next one's blocks before it stores (829 us: the
-// hardware's dealing balances better); a barrier a quadrant (853 us against 875,
-// before the loads were spread); all of a half's loads at once (875 us against
-// 807).
+// us, 2.5-2.6 PFLOP/s; 8192 x 8192 x 8192: 430 us, 2.56 PFLOP/s (a library's plain
+// 8-bit product reaches 2.71-2.78 there).  When the last round of tiles fills at
+// most half of the CUs, two workgroups take the halves of each (32768 rows: 747 ->
+// 740 us; 34000: 800 -> 769; 16500 by 4 experts of 4096 x 1536: 117 -> 109).
+// Measured and not kept: one workgroup a CU that walks the tiles and loads the
+// next one's blocks before it stores (829 us: the hardware's dealing balances
+// better); a barrier a quadrant (853 us against 875, before the loads were
+// spread); all of a half's loads at once (875 us against 807).
 __global__ __launch_bounds__(kMmThreads, 1) void expert_gemm_big_kernel(GemmArgs g, int32_t ntile,
                                                                         int32_t unit) {
   __shared__ __align__(16) uint8_t a00[kHalfBytes], a01[kHalfBytes], a10[kHalfBytes], a11[kHalfBytes];
@@ -327,9 +330,19 @@ __global__ __launch_bounds__(kMmThreads, 1) void expert_gemm_big_kernel(GemmArgs
   const int wv = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6)), wi = wv >> 1, wj = wv & 1;
   const int32_t mtile = row_tiles(g.off, g.ne, g.cap, unit);
   const int64_t tiles = static_cast<int64_t>(mtile) * ntile;
-  if (blockIdx.x >= tiles) return;
-  const Tile2 at = tile_order(blockIdx.x, tiles, mtile, ntile);
-  const RowTile rt = find_row_tile(g.off, g.ne, g.cap, unit, at.m);
+  // workgroups behind `whole` take half the rows of a tile
+  const int64_t left = tiles % kComputeUnits, whole = unit == kBigTile && left <= kComputeUnits / 2 ? tiles - left : tiles;
+  const bool split = blockIdx.x >= whole;
+  const int64_t t = split ? whole + ((blockIdx.x - whole) >> 1) : blockIdx.x;
+  if (t >= tiles) return;
+  const Tile2 at = tile_order(t, tiles, mtile, ntile);
+  RowTile rt = find_row_tile(g.off, g.ne, g.cap, unit, at.m);
+  if (split) {
+    const int32_t skip = (blockIdx.x - whole) & 1 ? 128 : 0;
+    rt.row0 += skip;
+    rt.rows = min(rt.rows - skip, 128);
+    if (rt.rows <= 0) return;
+  }
   const uint8_t* wp = g.w[rt.p];
   const uint8_t* ws = g.w_scale[rt.p];
   if (!usable(wp, ws)) return;
@@ -786,7 +799,7 @@ hipError_t launch_expert_gemm(const int32_t* off, int32_t ne, const uint8_t* q, 
   // for each of 6 experts of 4096 x 7168: 122 and 91; 5461: 1010 and 799.
   const auto rounds = [&](int32_t u) { return ((cap / u + ne / 2 + 1) * nbig + 255) / 256; };
   const int32_t unit = 11 * rounds(128) < 15 * rounds(256) ? 128 : 256;
-  const int64_t tiles = (cap / unit + ne) * nbig;
+  const int64_t tiles = (cap / unit + ne) * nbig + (unit == kBigTile ? kComputeUnits / 2 : 0);
   hipLaunchKernelGGL(expert_gemm_big_kernel, dim3(static_cast<uint32_t>(tiles)), dim3(kMmThreads), 0, st, g, nbig, unit);
   return hipGetLastError();
 }

@@ -253,7 +253,9 @@ def test_expert_gemm_real_values(N, K, loads):
     assert (np.abs(got - want) <= slack + BF16_STEP * (np.abs(want) + slack)).all()
 
 
-@pytest.mark.parametrize("loads,N,K", [([700, 0, 300, 211], 8200, 392), ([130, 257, 1000], 6152, 1160)])
+@pytest.mark.parametrize("loads,N,K", [([700, 0, 300, 211], 8200, 392), ([130, 257, 1000], 6152, 1160),
+                                       # the last 41 and 69 tiles go to two workgroups each
+                                       ([1000, 795, 5], 8200, 392), ([2600, 300], 6152, 264)])
 def test_expert_gemm_tiles_of_256_rows(loads, N, K):
     """Enough tiles for the full height; ragged rows, columns and blocks, and blocks left over from four."""
     say(f"expert_gemm 256-row tiles loads={loads} N={N} K={K}")
