@@ -58,6 +58,21 @@ constexpr int kBigTile = 256;        // rows of either operand
 constexpr int kComputeUnits = 256;
 constexpr int kHalfBytes = 128 * 128;  // half of an operand's block of 128, in LDS
 
+// Workgroup b's share of `tiles` tiles: tile t's rows skip..skip + rows - 1.  A last
+// round that fills at most half of the CUs has two workgroups for each of its
+// tiles, if they may be halved: tiles + kComputeUnits / 2 workgroups suffice, and
+// those that have none get a t of `tiles` and more.
+struct TileShare {
+  int64_t t;
+  int32_t skip, rows;
+};
+
+__device__ __forceinline__ TileShare share_tile(int64_t b, int64_t tiles, bool halves) {
+  const int64_t left = tiles % kComputeUnits, whole = halves && left <= kComputeUnits / 2 ? tiles - left : tiles;
+  if (b < whole) return TileShare{b, 0, kBigTile};
+  return TileShare{whole + ((b - whole) >> 1), (b - whole) & 1 ? 128 : 0, 128};
+}
+
 // One operand of a tile: row r of block b at base + min(r, last) * row_pitch +
 // b * block_pitch, 128 bytes.
 struct BigOperand {
@@ -330,19 +345,13 @@ __global__ __launch_bounds__(kMmThreads, 1) void expert_gemm_big_kernel(GemmArgs
   const int wv = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6)), wi = wv >> 1, wj = wv & 1;
   const int32_t mtile = row_tiles(g.off, g.ne, g.cap, unit);
   const int64_t tiles = static_cast<int64_t>(mtile) * ntile;
-  // workgroups behind `whole` take half the rows of a tile
-  const int64_t left = tiles % kComputeUnits, whole = unit == kBigTile && left <= kComputeUnits / 2 ? tiles - left : tiles;
-  const bool split = blockIdx.x >= whole;
-  const int64_t t = split ? whole + ((blockIdx.x - whole) >> 1) : blockIdx.x;
-  if (t >= tiles) return;
-  const Tile2 at = tile_order(t, tiles, mtile, ntile);
+  const TileShare share = share_tile(blockIdx.x, tiles, unit == kBigTile);
+  if (share.t >= tiles) return;
+  const Tile2 at = tile_order(share.t, tiles, mtile, ntile);
   RowTile rt = find_row_tile(g.off, g.ne, g.cap, unit, at.m);
-  if (split) {
-    const int32_t skip = (blockIdx.x - whole) & 1 ? 128 : 0;
-    rt.row0 += skip;
-    rt.rows = min(rt.rows - skip, 128);
-    if (rt.rows <= 0) return;
-  }
+  rt.row0 += share.skip;
+  rt.rows = min(rt.rows - share.skip, share.rows);
+  if (rt.rows <= 0) return;
   const uint8_t* wp = g.w[rt.p];
   const uint8_t* ws = g.w_scale[rt.p];
   if (!usable(wp, ws)) return;
@@ -546,10 +555,11 @@ __device__ __forceinline__ void widen_half(i32x4& y, const i32x2v& raw, float sc
   y[2 * HALF + 1] = hi;
 }
 
-// A block of 128 is 32 steps n = 8 g + i: A's fragment i by B's eight, over the
-// g-th eight of each lane's 32 values.  During step n the fragment of A for step
-// n + 1 and fragment i of B for the next g are widened, an instruction or two
-// behind each product, from bytes read from LDS four steps before.
+// A block of 128 is 32 steps n = 8 g + i: A's fragment i by B's J (eight, or the
+// four of its first half), over the g-th eight of each lane's 32 values.  During
+// step n the fragment of A for step n + 1 and fragment i of B for the next g are
+// widened, an instruction or two behind each product, from bytes read from LDS
+// four steps before.
 struct WideState {
   i32x4 a[2];     // A's fragment of this step and of the next
   i32x4 b[2][8];  // B's of this g and of the next
@@ -577,7 +587,8 @@ __device__ __forceinline__ int scale_byte(const uint8_t* s, int32_t row, int32_t
 // Block k in LDS buffers [half] of its parity; n_*: the other parity's, where
 // block k + 1 is or arrives.  B's halves are read up to step 19 and A's up to
 // step 26; behind the barriers there the loads of block k + 2 go into them, 32
-// steps (about 4100 cycles of products) before they are read.
+// steps (about 4100 cycles of products with J = 8) before they are read.
+template <int J>
 __device__ __forceinline__ void wide_block(const WideTile& t, WideState& w, int32_t k, int32_t blocks, uint8_t* al,
                                            uint8_t* ah, uint8_t* bl, uint8_t* bh, uint8_t* nal, uint8_t* nah, uint8_t* nbl,
                                            uint8_t* nbh, f32x4 (&acc)[8][8]) {
@@ -589,41 +600,91 @@ __device__ __forceinline__ void wide_block(const WideTile& t, WideState& w, int3
 #pragma unroll
   for (int n = 0; n < 32; ++n) {
     const int g = n >> 3, i = n & 7;
-    if (n == 20 || n == 27) meet<8>();
+    if (n == 20) meet<8>();
+    if (n == 27) meet<J>();
     if (n == 24) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) w.sb[j] = scale_of(w.nb[j]);
+      for (int j = 0; j < J; ++j) w.sb[j] = scale_of(w.nb[j]);
     }
     if (n == 31) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) w.sa[j] = scale_of(w.na[j]);
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < J; ++j) {
       product_wide(acc[i][j], w.a[n & 1], w.b[g & 1][j]);
       if (j == 0) widen_half<0>(w.a[(n + 1) & 1], w.raw_a[(n + 1) & 3], w.sa[(n + 1) & 7]);
       if (j == 1) widen_half<1>(w.a[(n + 1) & 1], w.raw_a[(n + 1) & 3], w.sa[(n + 1) & 7]);
-      if (j == 2) widen_half<0>(w.b[(g + 1) & 1][i], w.raw_b[n & 3], w.sb[i]);
-      if (j == 3) widen_half<1>(w.b[(g + 1) & 1][i], w.raw_b[n & 3], w.sb[i]);
-      if (j == 4) {
+      if (j == 2 && i < J) widen_half<0>(w.b[(g + 1) & 1][i], w.raw_b[n & 3], w.sb[i]);
+      if (j == 3 && i < J) widen_half<1>(w.b[(g + 1) & 1][i], w.raw_b[n & 3], w.sb[i]);
+      if (j == J / 2) {  // behind the last use of the bytes it replaces
         const int m = n + 5;
         w.raw_a[m & 3] = m < 32 ? read_raw(al, ah, t.at_a[(m >> 3) & 3], m & 7)
                                 : read_raw(nal, nah, t.at_a[0], m & 7);
       }
-      if (j == 5) {
+      if (j == J / 2 + 1 && ((n + 4) & 7) < J) {
         const int m = n + 4;  // widened at step m for g + 1
         w.raw_b[m & 3] = m < 24 ? read_raw(bl, bh, t.at_b[((m >> 3) + 1) & 3], m & 7)
                                 : read_raw(nbl, nbh, t.at_b[((m >> 3) + 1) & 3], m & 7);
       }
-      if (j == 6 || j == 7) {
-        if (n >= 2 && n < 10) {
-          if (j == 6) w.na[n - 2] = scale_byte(sa, b_row(t.wi, n - 2, t.l16), t.a.last);
-          if (j == 7) w.nb[n - 2] = scale_byte(sb, b_row(t.wj, n - 2, t.l16), t.b.last);
-        }
-        if (n >= 20 && n < 24) (j == 6 ? load_bl : load_bh).issue(n - 20);
-        if (n >= 27 && n < 31) (j == 6 ? load_al : load_ah).issue(n - 27);
+      if (j == J - 2) {
+        if (n >= 2 && n < 10) w.na[n - 2] = scale_byte(sa, b_row(t.wi, n - 2, t.l16), t.a.last);
+        if (n >= 20 && n < 24) load_bl.issue(n - 20);
+        if (n >= 27 && n < 31) load_al.issue(n - 27);
+      }
+      if (j == J - 1) {
+        if (n >= 2 && n < 2 + J) w.nb[n - 2] = scale_byte(sb, b_row(t.wj, n - 2, t.l16), t.b.last);
+        if (J == 8 && n >= 20 && n < 24) load_bh.issue(n - 20);
+        if (n >= 27 && n < 31) load_ah.issue(n - 27);
       }
     }
+  }
+}
+
+// All blocks of a tile; LDS buffers [block parity][half].
+template <int J>
+__device__ __forceinline__ void wide_tile(const WideTile& t, int32_t blocks, uint8_t* a00, uint8_t* a01, uint8_t* a10,
+                                          uint8_t* a11, uint8_t* b00, uint8_t* b01, uint8_t* b10, uint8_t* b11,
+                                          f32x4 (&acc)[8][8]) {
+  WideState w;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    w.sa[j] = scale_of(scale_byte(t.scale_a, b_row(t.wi, j, t.l16), t.a.last));
+    if (j < J) w.sb[j] = scale_of(scale_byte(t.scale_b, b_row(t.wj, j, t.l16), t.b.last));
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    asm volatile("" : "+v"(w.sa[j]));
+    if (j < J) asm volatile("" : "+v"(w.sb[j]));
+  }
+  load_half(t.b, 0, blocks, t.off_b[0], b00);
+  if (J == 8) load_half(t.b, 0, blocks, t.off_b[1], b01);
+  load_half(t.a, 0, blocks, t.off_a[0], a00);
+  load_half(t.a, 0, blocks, t.off_a[1], a01);
+  load_half(t.b, 1, blocks, t.off_b[0], b10);
+  if (J == 8) load_half(t.b, 1, blocks, t.off_b[1], b11);
+  load_half(t.a, 1, blocks, t.off_a[0], a10);
+  load_half(t.a, 1, blocks, t.off_a[1], a11);
+  meet<8 + J>();
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const i32x2v raw = read_raw(b00, b01, t.at_b[0], j);
+    widen_half<0>(w.b[0][j], raw, w.sb[j]);
+    widen_half<1>(w.b[0][j], raw, w.sb[j]);
+  }
+  const i32x2v raw = read_raw(a00, a01, t.at_a[0], 0);
+  widen_half<0>(w.a[0], raw, w.sa[0]);
+  widen_half<1>(w.a[0], raw, w.sa[0]);
+#pragma unroll
+  for (int m = 0; m < 4; ++m) {
+    w.raw_a[(m + 1) & 3] = read_raw(a00, a01, t.at_a[0], m + 1);
+    w.raw_b[m] = read_raw(b00, b01, t.at_b[1], m);
+  }
+  asm volatile("s_nop 1");
+  for (int32_t k = 0; k < blocks; k += 2) {
+    wide_block<J>(t, w, k, blocks, a00, a01, b00, b01, a10, a11, b10, b11, acc);
+    wide_block<J>(t, w, k + 1, blocks, a10, a11, b10, b11, a00, a01, b00, b01, acc);
+    products_done();
   }
 }
 
@@ -660,6 +721,9 @@ __device__ __forceinline__ int32_t expert_of_rank(const int32_t* off, int32_t ne
 // us, and against that: 1200 without the loads (a bound, not a result), 2260 with
 // the tiles dealt to the XCDs in one walk over all experts (an XCD got whole
 // experts), 1404 with the widening spread over all eight products of a step.
+// Tiles of at most 128 rows of dy, the halves of a last round's among them,
+// multiply four fragments of B instead of eight (4 experts of 512 x 1024 from 3000
+// rows: 34 -> 23 us; 8 of 1408 x 2048 from 9000: 67 -> 63-68).
 __global__ __launch_bounds__(kMmThreads, 1) void expert_wgrad_big_kernel(
     const int32_t* off, int32_t ne, const uint8_t* dyt, const uint8_t* dyt_scale, int32_t N, const uint8_t* xt,
     const uint8_t* xt_scale, int32_t K, int64_t cap, float* const* grads, bool accumulate, int32_t ntile,
@@ -670,8 +734,11 @@ __global__ __launch_bounds__(kMmThreads, 1) void expert_wgrad_big_kernel(
   const int wv = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6)), wi = wv >> 1, wj = wv & 1;
   // every expert's tiles are dealt to all XCDs (experts differ in rows, so an
   // XCD must not get whole ones), the expert with the most rows first
-  const int32_t per = ntile * ktile, turn = static_cast<int32_t>(blockIdx.x) / per;
-  const Tile2 at = tile_order(blockIdx.x - turn * per, per, ntile, ktile);
+  const int32_t per = ntile * ktile;
+  const TileShare share = share_tile(blockIdx.x, static_cast<int64_t>(ne) * per, true);
+  const int32_t turn = static_cast<int32_t>(share.t / per);
+  if (turn >= ne) return;
+  const Tile2 at = tile_order(share.t - static_cast<int64_t>(turn) * per, per, ntile, ktile);
   const int32_t p = expert_of_rank(off, ne, cap, turn), tn = at.m, tk = at.n;
   float* out = grads[p];
   if (out == nullptr) return;
@@ -679,7 +746,9 @@ __global__ __launch_bounds__(kMmThreads, 1) void expert_wgrad_big_kernel(
   const int32_t blocks = max(ceil_div(o1 - o0, kQBlock), 0);
   if (blocks == 0 && accumulate) return;
   const int64_t first = o0 / kQBlock + p;
-  const int32_t n0 = tn * kBigTile, k0 = tk * kBigTile, rows = min(N - n0, kBigTile), cols = min(K - k0, kBigTile);
+  const int32_t n0 = tn * kBigTile + share.skip, k0 = tk * kBigTile;
+  const int32_t rows = min(N - n0, share.rows), cols = min(K - k0, kBigTile);
+  if (rows <= 0) return;
   f32x4 acc[8][8];
 #pragma unroll
   for (int i = 0; i < 8; ++i)
@@ -708,43 +777,10 @@ __global__ __launch_bounds__(kMmThreads, 1) void expert_wgrad_big_kernel(
       t.at_a[g] = (wi * 64 + l16) * 128 + part;
       t.at_b[g] = (wj * 64 + l16) * 128 + part;
     }
-    WideState w;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      w.sa[j] = scale_of(scale_byte(t.scale_a, b_row(wi, j, l16), t.a.last));
-      w.sb[j] = scale_of(scale_byte(t.scale_b, b_row(wj, j, l16), t.b.last));
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) asm volatile("" : "+v"(w.sa[j]), "+v"(w.sb[j]));
-    load_half(t.b, 0, blocks, t.off_b[0], b00);
-    load_half(t.b, 0, blocks, t.off_b[1], b01);
-    load_half(t.a, 0, blocks, t.off_a[0], a00);
-    load_half(t.a, 0, blocks, t.off_a[1], a01);
-    load_half(t.b, 1, blocks, t.off_b[0], b10);
-    load_half(t.b, 1, blocks, t.off_b[1], b11);
-    load_half(t.a, 1, blocks, t.off_a[0], a10);
-    load_half(t.a, 1, blocks, t.off_a[1], a11);
-    meet<16>();
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const i32x2v raw = read_raw(b00, b01, t.at_b[0], j);
-      widen_half<0>(w.b[0][j], raw, w.sb[j]);
-      widen_half<1>(w.b[0][j], raw, w.sb[j]);
-    }
-    const i32x2v raw = read_raw(a00, a01, t.at_a[0], 0);
-    widen_half<0>(w.a[0], raw, w.sa[0]);
-    widen_half<1>(w.a[0], raw, w.sa[0]);
-#pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      w.raw_a[(m + 1) & 3] = read_raw(a00, a01, t.at_a[0], m + 1);
-      w.raw_b[m] = read_raw(b00, b01, t.at_b[1], m);
-    }
-    asm volatile("s_nop 1");
-    for (int32_t k = 0; k < blocks; k += 2) {
-      wide_block(t, w, k, blocks, a00, a01, b00, b01, a10, a11, b10, b11, acc);
-      wide_block(t, w, k + 1, blocks, a10, a11, b10, b11, a00, a01, b00, b01, acc);
-      products_done();
-    }
+    if (rows > 128)
+      wide_tile<8>(t, blocks, a00, a01, a10, a11, b00, b01, b10, b11, acc);
+    else
+      wide_tile<4>(t, blocks, a00, a01, a10, a11, b00, b01, b10, b11, acc);
   }
   const bool vec = (reinterpret_cast<uintptr_t>(out) & 15) == 0;
   // a fragment of rows at a time through the wave's own piece of LDS, so that a
@@ -755,6 +791,7 @@ __global__ __launch_bounds__(kMmThreads, 1) void expert_wgrad_big_kernel(
   meet<0>();  // LDS is free: the last loads (zeros) have arrived, the reads are done
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
+    if (128 * (j >> 2) >= rows) break;
 #pragma unroll
     for (int i = 0; i < 8; ++i) *reinterpret_cast<f32x4*>(stage + l16 * 528 + 64 * i + 16 * kg) = acc[i][j];
 #pragma unroll
@@ -809,7 +846,7 @@ hipError_t launch_expert_wgrad(const int32_t* off, int32_t ne, const uint8_t* dy
                                bool accumulate, hipStream_t st) {
   if (ne == 0) return hipSuccess;
   const int32_t ntile = ceil_div(N, kBigTile), ktile = ceil_div(K, kBigTile);
-  hipLaunchKernelGGL(expert_wgrad_big_kernel, dim3(static_cast<uint32_t>(ne * ntile * ktile)), dim3(kMmThreads), 0, st, off,
+  hipLaunchKernelGGL(expert_wgrad_big_kernel, dim3(static_cast<uint32_t>(ne * ntile * ktile + kComputeUnits / 2)), dim3(kMmThreads), 0, st, off,
                      ne, dyt, dyt_scale, N, xt, xt_scale, K, cap, grads, accumulate, ntile, ktile);
   return hipGetLastError();
 }

@@ -342,7 +342,9 @@ def columns(rng, seg, width, whole):
 @pytest.mark.parametrize("shift", [0, 1])
 @pytest.mark.parametrize("loads,N,K", [([1], 8, 8), ([127, 1, 0, 129, 257], 136, 72), ([300, 0, 40], 264, 520),
                                        ([1] * 40 + [0] * 30 + [130], 72, 136), ([640], 384, 256),
-                                       ([129, 385, 0, 513], 776, 520)])
+                                       ([129, 385, 0, 513], 776, 520),
+                                       # whole tiles; whole ones and 14 that two workgroups share
+                                       ([300, 1, 0, 513], 1160, 2056), ([129, 257, 0, 40, 128, 500], 1288, 2056)])
 def test_expert_wgrad_whole_numbers(loads, N, K, shift, accumulate):
     say(f"expert_wgrad loads={loads[:8]} N={N} K={K} shift={shift} accumulate={accumulate}")
     rng = np.random.default_rng([N, K, sum(loads)])
@@ -363,10 +365,10 @@ def test_expert_wgrad_whole_numbers(loads, N, K, shift, accumulate):
     assert (store[:shift] == 3.0).all() and (store[shift + seg.ne * N * K:] == 3.0).all()
 
 
-def test_expert_wgrad_real_values():
+@pytest.mark.parametrize("N,K", [(136, 264), (1288, 2056)])
+def test_expert_wgrad_real_values(N, K):
     rng = np.random.default_rng(12)
     seg = Segment([700, 0, 33, 129], p0=1)
-    N, K = 136, 264
     dyt, dys = columns(rng, seg, N, False)
     xt, xs = columns(rng, seg, K, False)
     g = torch.empty(seg.ne, N, K, device=DEV)
