@@ -188,10 +188,15 @@ __global__ __launch_bounds__(kGradThreads) void grad_sumsq_kernel(const void* co
   if (threadIdx.x == 0) partial[blockIdx.x] = s;
 }
 
+// m: kGradBlocks partial sums, or none.
 __global__ __launch_bounds__(kGradThreads) void grad_total_kernel(const double* __restrict__ partial, int32_t m,
                                                                   double* __restrict__ sumsq, bool accumulate) {
-  double acc = 0.0;
-  for (int32_t i = threadIdx.x; i < m; i += kGradThreads) acc += partial[i];
+  double part[kGradBlocks / kGradThreads], acc = 0.0;  // all loads at once
+#pragma unroll
+  for (int i = 0; i < kGradBlocks / kGradThreads; ++i)
+    part[i] = m > 0 ? partial[i * kGradThreads + static_cast<int>(threadIdx.x)] : 0.0;
+#pragma unroll
+  for (int i = 0; i < kGradBlocks / kGradThreads; ++i) acc += part[i];
   const double s = block_sum_f64(acc);
   if (threadIdx.x == 0) *sumsq = accumulate ? *sumsq + s : s;
 }
@@ -203,11 +208,12 @@ __global__ __launch_bounds__(kGradThreads) void grad_clip_kernel(const void* con
                                                                  float* __restrict__ norm_out, void* const* __restrict__ out) {
   extern __shared__ int32_t s_first[];
   constexpr int kSize = BF16 ? 2 : 4, kVec = 16 / kSize, kChunk = kGradBytes / kSize;
-  const double norm = sqrt(*sumsq), ratio = max_norm / (norm + 1e-6);
+  const double square_sum = *sumsq;
+  const Walk w = grad_walk(tensors, numels, n, kChunk, s_first);
+  const double norm = sqrt(square_sum), ratio = max_norm / (norm + 1e-6);
   const double coef = ratio >= 1.0 ? 1.0 : ratio;  // NaN stays NaN; fp64, since a huge norm's factor is below fp32's range
   if (blockIdx.x == 0 && threadIdx.x == 0 && norm_out != nullptr) *norm_out = static_cast<float>(norm);
   if (coef == 1.0 && out == nullptr) return;
-  const Walk w = grad_walk(tensors, numels, n, kChunk, s_first);
   Chunk x, next;
   const int32_t blocks = static_cast<int32_t>(gridDim.x);
   if (static_cast<int32_t>(blockIdx.x) < w.total) next = chunk_at(w, static_cast<int32_t>(blockIdx.x), 0, kChunk, kSize);
