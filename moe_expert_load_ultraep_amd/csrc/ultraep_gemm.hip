@@ -453,7 +453,7 @@ __global__ __launch_bounds__(kMmThreads, 1) void expert_gemm_big_kernel(GemmArgs
 // ------------------------------------------------------------------------
 constexpr int kThinWaves = 4;
 constexpr int kThinThreads = 64 * kThinWaves;
-constexpr int kThinRows = 16, kThinCols = 32;
+constexpr int kThinRows = 32, kThinCols = 32;
 
 // Fragment of 16 rows: lane's two 16-byte parts kg and kg + 4 of its row, so
 // that one load covers 64 bytes of each row in order.  Both operands take the
@@ -463,61 +463,89 @@ __device__ __forceinline__ i32x8 thin_fragment(const uint8_t* row) {
                                  4, 5, 6, 7);
 }
 
-// 32 weight rows by 16 rows.  The four waves split the blocks of 128
+// 32 weight rows by 16 or 32 rows.  The four waves split the blocks of 128
 // (wave v takes v, v + 4, ...), every weight byte goes from memory to the
 // registers of the one wave that uses it, the next block's while this one is
 // multiplied, and the waves' sums meet in LDS and are added in wave order.
 // Bound by HBM: 41 rows by 6 experts of 4096 x 7168 (177 MB) take 34-37 us, 4.8-5.2
-// TB/s, the rate of a large copy.  With 64 columns a tile 36-38 us with four
-// waves, 38 with two or eight; 128 columns 43; loads two blocks ahead are slower
-// (fewer waves fit), as are non-temporal loads (46 us).
-__global__ __launch_bounds__(kThinThreads) void expert_gemm_thin_kernel(GemmArgs g, int32_t ntile) {
-  constexpr int FN = kThinCols / 16;
-  __shared__ __align__(16) float s_sum[kThinWaves][kThinRows][kThinCols + 4];
+// TB/s, the rate of a large copy.  Tiles of 16 rows alone read an expert's weights
+// twice as often: 96 rows 55 us instead of 49, 128 rows of one expert 46 instead of
+// 32.  With 64 columns a tile 36-38 us with four waves, 38 with two or eight; 128
+// columns 43; loads two blocks ahead are slower (fewer waves fit), as are
+// non-temporal loads (46 us).
+constexpr int kThinFrags = kThinCols / 16;
+struct ThinSums {
+  float v[kThinWaves][kThinRows][kThinCols + 4];
+};
+
+// One wave's part of a tile of up to 16 * FR rows.
+template <int FR>
+__device__ __forceinline__ void thin_tile(const GemmArgs& g, const RowTile& rt, const uint8_t* wp, const uint8_t* ws, int32_t n0,
+                                          int32_t cols, int wv, ThinSums& sums) {
+  constexpr int FN = kThinFrags;
   const int32_t Kp = q_pitch(g.K), Ks = s_pitch(g.K), blocks = Kp / 128;
   const int lane = lane_id(), l16 = lane & 15, kg = lane >> 4;
+  const uint8_t *pa[FN], *pb[FR], *sb[FR];
+#pragma unroll
+  for (int i = 0; i < FN; ++i) pa[i] = wp + static_cast<int64_t>(n0 + min(16 * i + l16, cols - 1)) * Kp + kg * 16;
+#pragma unroll
+  for (int i = 0; i < FR; ++i) {
+    const int64_t r = rt.row0 + min(16 * i + l16, rt.rows - 1);
+    pb[i] = g.q + r * Kp + kg * 16;
+    sb[i] = g.q_scale + r * Ks;
+  }
+  const uint8_t* sa = ws + static_cast<int64_t>(n0 / 128) * Ks;
+  f32x4 acc[FN][FR];
+#pragma unroll
+  for (int i = 0; i < FN; ++i)
+#pragma unroll
+    for (int j = 0; j < FR; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  i32x8 fa[FN], fb[FR];
+  int xa, xb[FR];
+  const auto load = [&](int32_t block) {
+    const int32_t b = min(block, blocks - 1);
+#pragma unroll
+    for (int i = 0; i < FN; ++i) fa[i] = thin_fragment(pa[i] + b * 128);
+#pragma unroll
+    for (int i = 0; i < FR; ++i) fb[i] = thin_fragment(pb[i] + b * 128);
+    xa = sa[b];
+#pragma unroll
+    for (int i = 0; i < FR; ++i) xb[i] = sb[i][b];
+  };
+  load(wv);
+  for (int32_t b = wv; b < blocks; b += kThinWaves) {
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+      for (int j = 0; j < FR; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fa[i], fb[j], acc[i][j], 0, 0, 0, xa, 0, xb[j]);
+    load(b + kThinWaves);
+  }
+#pragma unroll
+  for (int i = 0; i < FN; ++i)
+#pragma unroll
+    for (int j = 0; j < FR; ++j) *reinterpret_cast<f32x4*>(&sums.v[wv][16 * j + l16][16 * i + 4 * kg]) = acc[i][j];
+}
+
+__global__ __launch_bounds__(kThinThreads) void expert_gemm_thin_kernel(GemmArgs g, int32_t ntile, int32_t unit) {
+  __shared__ __align__(16) ThinSums s_sum;
   const int wv = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
-  const int32_t mtile = row_tiles(g.off, g.ne, g.cap, kThinRows);
+  const int32_t mtile = row_tiles(g.off, g.ne, g.cap, unit);
   const int64_t tiles = static_cast<int64_t>(mtile) * ntile;
   for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
     const int64_t full = tiles & ~int64_t{7};
     const int64_t at = t < full ? (t & 7) * (full >> 3) + (t >> 3) : t;  // an XCD's tiles follow each other
     const int32_t tn = static_cast<int32_t>(at / mtile), tm = static_cast<int32_t>(at - static_cast<int64_t>(tn) * mtile);
-    const RowTile rt = find_row_tile(g.off, g.ne, g.cap, kThinRows, tm);
+    const RowTile rt = find_row_tile(g.off, g.ne, g.cap, unit, tm);
     const uint8_t* wp = g.w[rt.p];
     const uint8_t* ws = g.w_scale[rt.p];
     if (!usable(wp, ws)) continue;
     const int32_t n0 = tn * kThinCols, cols = min(g.N - n0, kThinCols);
-    const uint8_t* pa[FN];
-#pragma unroll
-    for (int i = 0; i < FN; ++i) pa[i] = wp + static_cast<int64_t>(n0 + min(16 * i + l16, cols - 1)) * Kp + kg * 16;
-    const int64_t r = rt.row0 + min(l16, rt.rows - 1);
-    const uint8_t* pb = g.q + r * Kp + kg * 16;
-    const uint8_t* sa = ws + static_cast<int64_t>(n0 / 128) * Ks;
-    const uint8_t* sb = g.q_scale + r * Ks;
-    f32x4 acc[FN];
-#pragma unroll
-    for (int i = 0; i < FN; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    i32x8 fa[FN], fb;
-    int xa, xb;
-    const auto load = [&](int32_t block) {
-      const int32_t b = min(block, blocks - 1);
-#pragma unroll
-      for (int i = 0; i < FN; ++i) fa[i] = thin_fragment(pa[i] + b * 128);
-      fb = thin_fragment(pb + b * 128);
-      xa = sa[b];
-      xb = sb[b];
-    };
-    load(wv);
-    for (int32_t b = wv; b < blocks; b += kThinWaves) {
-#pragma unroll
-      for (int i = 0; i < FN; ++i)
-        acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fa[i], fb, acc[i], 0, 0, 0, xa, 0, xb);
-      load(b + kThinWaves);
-    }
-    __syncthreads();  // the previous tile's sums have been read
-#pragma unroll
-    for (int i = 0; i < FN; ++i) *reinterpret_cast<f32x4*>(&s_sum[wv][l16][16 * i + 4 * kg]) = acc[i];
+    if (t >= gridDim.x) __syncthreads();  // the previous tile's sums have been read
+    if (rt.rows <= 16)
+      thin_tile<1>(g, rt, wp, ws, n0, cols, wv, s_sum);
+    else
+      thin_tile<2>(g, rt, wp, ws, n0, cols, wv, s_sum);
     __syncthreads();
     // two columns a thread
     for (int u = threadIdx.x; u < kThinRows * kThinCols / 2; u += kThinThreads) {
@@ -526,8 +554,8 @@ __global__ __launch_bounds__(kThinThreads) void expert_gemm_thin_kernel(GemmArgs
       float lo = 0.f, hi = 0.f;
 #pragma unroll
       for (int v = 0; v < kThinWaves; ++v) {
-        lo += s_sum[v][row][c];
-        hi += s_sum[v][row][c + 1];
+        lo += s_sum.v[v][row][c];
+        hi += s_sum.v[v][row][c + 1];
       }
       *reinterpret_cast<uint32_t*>(g.out + (rt.row0 + row) * g.N + n0 + c) = pack_bf16(lo, hi);
     }
@@ -814,19 +842,24 @@ hipError_t launch_expert_gemm(const int32_t* off, int32_t ne, const uint8_t* q, 
   const GemmArgs g{off, ne, q, q_scale, K, w, w_scale, N, out, cap};
   const int32_t nbig = ceil_div(N, kBigTile);
   // Few rows.  Thin tiles take each row tile's weights from memory at 5.2 TB/s,
-  // cap / 16 + ne / 2 or so row tiles; big ones 0.8 us a block of 128 of K and
+  // cap / 32 + ne / 2 or so row tiles; big ones 0.8 us a block of 128 of K and
   // more the more of them share the memory, whatever the rows.  Both grow with
   // K alike, which leaves a bound on rows and N; and up to four rows an expert
   // nearly every thin tile is its expert's only one.  Thin / big, us: 6 experts of
-  // 4096 x 7168 at 1, 4, 8, 12, 16, 24 rows an expert 23/48, 34/52, 38/55, 46/55,
-  // 55/57, 66/58; 24 of 2048 x 5120 at 1, 4, 8: 32/45, 50/51, 61/52; 32 of 7168 x
-  // 2048 at 1, 4, 8: 59/66, 86/87, 108/91; 4 of 1536 x 5120 at 16, 32, 50, 70: 16/31,
-  // 19/32, 27/32, 34/33; one of 4096 x 7168 at 64, 96, 128: 24/41, 36/41, 46/42; 8 of
-  // 1024 x 1024 at 32, 55: 9.3/11.2, 11.7/11.4; 16 of 512 x 2048 at 32, 50: 14/17, 18/17.
-  if (cap <= 4 * static_cast<int64_t>(ne) || (cap + 4 * static_cast<int64_t>(ne)) * N <= 420000) {
+  // 4096 x 7168 at 4, 16, 24, 33 rows an expert 34/53, 49/57, 60/58, 72/59; 24 of
+  // 2048 x 5120 at 4, 8, 12: 51/51, 60/52, 68/53; 32 of 7168 x 2048 at 4, 8: 85/87,
+  // 101/91; 4 of 1536 x 5120 at 16, 32, 70, 100: 15/31, 21/31, 30/32, 35/33; one of
+  // 4096 x 7168 at 16, 64, 128, 200: 14/40, 18/41, 32/41, 59/41; 8 of 1024 x 1024 at
+  // 32, 55, 100: 8.9/11.1, 11.7/11.4, 14.7/11.5; 2 of 7168 x 2048 at 16, 32, 64:
+  // 12/16, 16/16, 26/17.
+  if (cap <= 4 * static_cast<int64_t>(ne) || (cap + 8 * static_cast<int64_t>(ne)) * N <= 600000) {
     const int32_t ntile = ceil_div(N, kThinCols);
-    const int64_t tiles = (cap / kThinRows + ne) * ntile;
-    hipLaunchKernelGGL(expert_gemm_thin_kernel, dim3(mm_grid(tiles)), dim3(kThinThreads), 0, st, g, ntile);
+    // 32 rows a tile, or 16 where that makes too few tiles to keep the memory
+    // busy (32 rows of one expert of 4096 x 7168, 128 or 256 tiles: 18.7 and 14.5
+    // us; 64 rows, 256 or 512: 18.5 and 24.3)
+    const int32_t unit = (cap / kThinRows + ne / 2) * ntile < 192 ? 16 : kThinRows;
+    const int64_t tiles = (cap / unit + ne) * ntile;
+    hipLaunchKernelGGL(expert_gemm_thin_kernel, dim3(mm_grid(tiles)), dim3(kThinThreads), 0, st, g, ntile, unit);
     return hipGetLastError();
   }
   // Rows a tile, 256 or 128: a tile of 128 takes about 11/15 of the time of one of

@@ -281,6 +281,17 @@ def test_expert_gemm_tiles_of_128_rows(loads, N, K):
     assert (got[seg.rows:] == 0x7FC1).all()
 
 
+@pytest.mark.parametrize("N,K", [(520, 264), (488, 8), (648, 1000)])
+def test_expert_gemm_thin_tiles_of_32_rows(N, K):
+    rng = np.random.default_rng([N, K, 32])
+    seg, q, qs, w, ws = operands(rng, [200, 0, 40, 3, 16, 17, 32, 33, 64], N, K, whole=True)
+    got = run_gemm(seg, q, qs, w, ws, N, K)
+    want, _ = to_bf16(X.expert_gemm(*gemm_values(seg, q, qs, w, ws), seg.off) + 0.0)
+    zero = lambda a: np.where(a == 0x8000, 0, a)  # noqa: E731
+    assert np.array_equal(zero(got[:seg.rows]), zero(want))
+    assert (got[seg.rows:] == 0x7FC1).all()
+
+
 @pytest.mark.parametrize("loads,N", [([200, 33, 300], 1544), ([700, 100], 4104)])
 def test_expert_gemm_large_tiles_real_values_missing_weights_and_nan(loads, N):
     rng = np.random.default_rng(N)
