@@ -393,6 +393,26 @@ def test_expert_wgrad_real_values(N, K):
         assert (np.abs(g[p].cpu().numpy() - want[p]) <= (max(n, 1) * F32_ADD) * mag[p]).all()
 
 
+def test_expert_wgrad_does_not_depend_on_the_other_experts():
+    """Whole tiles with six experts, shared ones with one: the same bits."""
+    rng = np.random.default_rng(14)
+    seg = Segment([300, 0, 33, 129, 260, 128], p0=1)
+    N, K = 1288, 2056
+    dyt, dys = columns(rng, seg, N, False)
+    xt, xs = columns(rng, seg, K, False)
+    d = [dev(a) for a in (dyt, dys, xt, xs)]
+    together, alone = torch.empty(seg.ne, N, K, device=DEV), torch.empty(seg.ne, N, K, device=DEV)
+    U.ultraep_expert_wgrad(seg.ctx, seg.plan, d[0], d[1], N, d[2], d[3], K, seg.p0, seg.p1, seg.rows,
+                           U.pointer_table(list(together)))
+    for p, b in enumerate(X.first_blocks(seg.off)[:-1]):
+        rows = seg.off[p + 1] - seg.off[p]
+        e = [t[b:b + U.quant_blocks(rows, 1)].contiguous() for t in d]
+        U.ultraep_expert_wgrad(seg.ctx, seg.plan, e[0], e[1], N, e[2], e[3], K, seg.p0 + p, seg.p0 + p + 1, rows,
+                               U.pointer_table([alone[p]]))
+    torch.cuda.synchronize()
+    assert torch.equal(together, alone)
+
+
 def grad_set(rng, sizes, bf16, shift):
     total = sum(sizes)
     x = rng.standard_normal(total).astype(np.float32) * 3
