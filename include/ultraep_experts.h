@@ -31,8 +31,8 @@
  * largest finite magnitude is at most 448 * 2^e (448 is e4m3's largest value;
  * e = 0 for a block of zeros or of nothing finite); q is the value times 2^-e,
  * rounded to nearest even.  Powers of two make that scaling exact, so the
- * rounding to e4m3 is the only one, and the matrix instructions take them
- * directly.  Infinities and NaN become NaN; they do not raise the scale.
+ * rounding to e4m3 is the only one, and a value of bf16's normal range is a bf16
+ * number.  Infinities and NaN become NaN; they do not raise the scale.
  *
  *   rows      q [rows][Hp], scale [rows][Hs]: a block is 128 columns of a row.
  *             Hp = H rounded up to 128, the columns behind H are zeros;
@@ -103,7 +103,11 @@ int ultraep_weight_quant(const ultraep_ctx* ctx, const uint16_t* const* weights,
 
 /* Multiply the rows of physical experts [p_begin, p_end) with their experts'
  * weights: out[i][n] = sum over k < K of x[i][k] * w_p[n][k] for the rows i of
- * expert p, the sums in fp32, rounded once to bf16 (nearest even).
+ * expert p, the products and sums in fp32, rounded once to bf16 (nearest even).
+ * Values are multiplied as bf16 numbers, exactly those the bytes and scales
+ * stand for, but magnitudes below 2^-126 may count as zero and such of 2^128
+ * and more as infinities.  The order of the sums, and so a row's last bits, go by
+ * K, N, capacity_rows and the number of experts; the same call gives the same bits.
  * In:  q, q_scale: capacity_rows rows of K columns in the rows form;
  *      w, w_scale: DEVICE arrays of p_end - p_begin device pointers, entry
  *      p - p_begin to expert p's weights (16-byte aligned) and scales (4-byte

@@ -1,18 +1,16 @@
 // gfx950 kernels of the experts' 8-bit products (include/ultraep_experts.h):
 // rows times weights for every physical expert of a segment, and the weight
 // gradients.  Both are sums over blocks of 128,
-//   C[i][j] = sum_b 2^(sa[i][b] + sb[j][b] - 254) * sum_{r < 128} A[i][b][r] * B[j][b][r],
-// which is what one V_MFMA_SCALE_F32_16X16X128 does with a scale byte a row of
-// either operand: the power-of-two scales cost no vector instruction.
+//   C[i][j] = sum_b sum_{r < 128} (2^(sa[i][b] - 127) * A[i][b][r]) * (2^(sb[j][b] - 127) * B[j][b][r]),
+// and both widen the bytes, scale included, to bf16 in the one instruction that
+// does it, which is exact, and multiply with V_MFMA_F32_16X16X32_BF16, whose
+// products and sums are fp32.
 //
-// Its precision, measured on the card: of eight products that a lane adds
+// The matrix instructions that take the bytes themselves are twice as fast, but
+// do not keep fp32 sums.  Measured on the card, V_MFMA_SCALE_F32_16X16X128_F8F6F4
+// and V_MFMA_F32_16X16X32_FP8_FP8 alike: of the eight products that a lane adds
 // together, every one is cut (towards zero) at 2^-13 of the largest one's power
-// of two; their sums and the accumulator are fp32.  The cuts come to 1.5e-5 of
-// the result on normal operands (2-norm), a hundredth of the bf16 rounding that
-// the rows products end in, so those use it: it is twice as fast as bf16.  The
-// weight gradients end in fp32 and may be added to for many steps: they widen
-// the bytes to bf16, scale included, which is exact, and multiply in bf16,
-// whose products and sums are fp32.
+// of two, so where large products cancel, the others beside them are lost.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -23,7 +21,6 @@
 namespace ultraep {
 namespace {
 
-typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kMmThreads = 256;
 
@@ -165,137 +162,191 @@ __device__ __forceinline__ void meet() {
   asm volatile("" ::: "memory");
 }
 
-// acc += A B of one 16 x 16 x 128 with byte BYTE of the scale words.  Written as
-// volatile asm for two reasons: the accumulator is updated where it is (with
-// the builtin the compiler picks another destination and moves whole
-// accumulators about, 460 moves in 256 products), and products and LDS reads
-// stay in the order of the source.  The s_nop covers a scale word or fragment
-// that a vector instruction wrote just before.
-template <int BYTE>
-__device__ __forceinline__ void product(f32x4& acc, const i32x8& a, const i32x8& b, int xa, int xb) {
-  if constexpr (BYTE == 0)
-    asm volatile("s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[0,0,0] op_sel_hi:[0,0,0]"
-                 : "+a"(acc) : "v"(a), "v"(b), "v"(xa), "v"(xb));
-  else if constexpr (BYTE == 1)
-    asm volatile("s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[1,1,0] op_sel_hi:[0,0,0]"
-                 : "+a"(acc) : "v"(a), "v"(b), "v"(xa), "v"(xb));
-  else if constexpr (BYTE == 2)
-    asm volatile("s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[0,0,0] op_sel_hi:[1,1,0]"
-                 : "+a"(acc) : "v"(a), "v"(b), "v"(xa), "v"(xb));
-  else
-    asm volatile("s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[1,1,0] op_sel_hi:[1,1,0]"
-                 : "+a"(acc) : "v"(a), "v"(b), "v"(xa), "v"(xb));
-}
-
 // Behind the products: their results are there before a vector instruction, a
 // copy the compiler makes included, reads them (19 wait states).  It stands in
 // the loop's own block, since copies start where the loop ends.
 __device__ __forceinline__ void products_done() { asm volatile("s_nop 15\n\ts_nop 3"); }
 
-// Fragment i of a half in LDS; at[h]: this lane's part h.
+typedef int i32x2v __attribute__((ext_vector_type(2)));
+
+// acc += A B of one 16 x 16 x 32 in bf16.  Written as volatile asm for two
+// reasons: the accumulator is updated where it is (with the builtin the compiler
+// picks another destination and moves whole accumulators about, 460 moves in 256
+// products), and products and LDS reads stay in the order of the source.  Nothing
+// that it reads is written by the two vector instructions before it.
+__device__ __forceinline__ void product_wide(f32x4& acc, const i32x4& a, const i32x4& b) {
+  asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
+}
+
+// Values 4 * HALF..4 * HALF + 3 of eight e4m3 bytes, times their scale, as bf16.
+template <int HALF>
+__device__ __forceinline__ void widen_half(i32x4& y, const i32x2v& raw, float scale) {
+  int lo, hi;
+  asm volatile("v_cvt_scalef32_pk_bf16_fp8 %0, %1, %2" : "=v"(lo) : "v"(raw[HALF]), "v"(scale));
+  asm volatile("v_cvt_scalef32_pk_bf16_fp8 %0, %1, %2 op_sel:[1,0,0]" : "=v"(hi) : "v"(raw[HALF]), "v"(scale));
+  y[2 * HALF] = lo;
+  y[2 * HALF + 1] = hi;
+}
+
+// A block of 128 is 32 steps n = 8 g + i: A's fragment i by B's J (eight, or the
+// four of its first half), over the g-th eight of each lane's 32 values.  During
+// step n the fragment of A for step n + 1 and fragment i of B for the next g are
+// widened, an instruction or two behind each product, from bytes read from LDS
+// four steps before.
+struct WideState {
+  i32x4 a[2];     // A's fragment of this step and of the next
+  i32x4 b[2][8];  // B's of this g and of the next
+  i32x2v raw_a[4], raw_b[4];
+  float sa[8], sb[8];  // scales of the block being widened
+  int na[8], nb[8];    // scale bytes of the next one
+};
+
+// ROWS (the rows products): A's fragments lie in PAIRS, its scale is one byte a
+// block for the wave's 128 rows, B's `scale_row` bytes a row; else (the weight
+// gradients) both operands' scales are a byte a row.
+struct WideTile {
+  BigOperand a, b;
+  const uint8_t *scale_a, *scale_b;  // scale bytes of the tile's rows (ROWS: A's of the wave's rows), block 0
+  int32_t pitch_a, pitch_b;          // scale bytes from a block to the next
+  int32_t scale_row;                 // ROWS: scale bytes from a row of B to the next
+  int32_t wi, wj, l16;
+  uint32_t off_a[2][4], off_b[2][4];
+  int at_a[4], at_b[4];              // LDS offset of this lane's eight bytes g, in a half
+};
+
+// LDS offsets of the eights.  Odd lanes of sixteen take the two eights of a part
+// the other way round, so that 32 lanes reading eight bytes meet all banks once.
 template <bool PAIRS>
-__device__ __forceinline__ i32x8 read_fragment(const uint8_t* lds, const int (&at)[2], int i) {
-  return __builtin_shufflevector(*reinterpret_cast<const i32x4*>(lds + at[0] + fragment_at<PAIRS>(i)),
-                                 *reinterpret_cast<const i32x4*>(lds + at[1] + fragment_at<PAIRS>(i)), 0, 1, 2, 3, 4, 5, 6, 7);
-}
-
-// A quarter of the wave's products: fragments a[4] by b[4], with the reads of
-// the four fragments f of half `lds` and the loads of another half among them: a
-// load's issue takes long enough for the matrix unit to run dry when several
-// follow each other.
-template <int I0, int J0, int BYTE, bool PAIRS>
-__device__ __forceinline__ void quadrant(const i32x8 (&a)[4], const i32x8 (&b)[4], int xa, const int (&xb)[8],
-                                         f32x4 (&acc)[8][8], const uint8_t* lds, const int (&at)[2], i32x8 (&f)[4], const HalfLoad& load) {
+__device__ __forceinline__ void read_offsets(WideTile& t) {
+  const int kg = lane_id() >> 4;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      product<BYTE>(acc[I0 + i][J0 + j], a[i], b[j], xa, xb[J0 + j]);
-      if (j == 0) f[i] = read_fragment<PAIRS>(lds, at, i);
-      if (j == 2) load.issue(i);
-    }
-}
-
-// Scale bytes of four blocks: one word for the wave's 128 rows of A, one a
-// fragment row of B.
-struct ScaleWords {
-  int a;
-  int b[8];
-};
-
-struct ScaleSource {
-  const uint8_t* a;  // the wave's row of weight scales
-  const uint8_t* b;  // the tile's first row of row scales
-  int32_t pitch;     // bytes a row
-  int32_t last;      // B's last row
-};
-
-__device__ __forceinline__ void load_scales(const ScaleSource& s, int32_t block, ScaleWords& w) {
-  const int wj = (threadIdx.x >> 6) & 1, m = lane_id() & 15;
-  w.a = *reinterpret_cast<const global_int*>(reinterpret_cast<uintptr_t>(s.a) + block);
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    w.b[j] = *reinterpret_cast<const int*>(s.b + static_cast<uint32_t>(min(b_row(wj, j, m), s.last)) * s.pitch + block);
-}
-
-// Waits for the words here, and not at their first use in the loop.
-__device__ __forceinline__ void settle(ScaleWords& w) {
-  asm volatile("" : "+v"(w.a));
-#pragma unroll
-  for (int j = 0; j < 8; ++j) asm volatile("" : "+v"(w.b[j]));
-}
-
-// LDS and registers of the pipeline.  Halves are indexed [block parity][half].
-struct Offsets {
-  uint32_t a[2][4], b[2][4];
-  int read_a[2], read_b[2];
-};
-
-// One block of 128, the U-th of four: the wave's 8 x 8 products of 16 x 16 x 128
-// in four quadrants, odd blocks walking B's halves the other way round.  Every
-// half is read once, in the quadrant before its first use, and the barrier
-// behind that quadrant frees it for the block after next: its loads have seven
-// quadrants (about 3600 cycles of products) to arrive, and 112 of the 128 KiB
-// are in flight or waiting at any time.
-template <int U>
-__device__ __forceinline__ void big_step(const BigOperand& a, const BigOperand& b, const Offsets& o, int32_t k,
-                                         int32_t blocks, uint8_t* alo, uint8_t* ahi, uint8_t* bx, uint8_t* by,
-                                         uint8_t* next_alo, uint8_t* next_by, i32x8 (&fal)[4], i32x8 (&fah)[4],
-                                         i32x8 (&fbx)[4], i32x8 (&fby)[4], const ScaleSource& ss, ScaleWords& sw,
-                                         ScaleWords& sn, f32x4 (&acc)[8][8]) {
-  constexpr int X = U & 1, Y = 1 - X;
-  meet<16>();
-  quadrant<0, 4 * X, U, false>(fal, fbx, sw.a, sw.b, acc, by, o.read_b, fby, HalfLoad(a, k + 2, blocks, o.a[0], alo));
-  quadrant<0, 4 * Y, U, true>(fal, fby, sw.a, sw.b, acc, ahi, o.read_a, fah, HalfLoad(b, k + 2, blocks, o.b[X], bx));
-  meet<16>();
-  if (U == 2) load_scales(ss, min(k + 2, blocks - 1) & ~3, sn);
-  quadrant<4, 4 * Y, U, true>(fah, fby, sw.a, sw.b, acc, next_alo, o.read_a, fal,
-                                  HalfLoad(b, k + 2, blocks, o.b[Y], by));
-  quadrant<4, 4 * X, U, false>(fah, fbx, sw.a, sw.b, acc, next_by, o.read_b, fby,
-                                  HalfLoad(a, k + 2, blocks, o.a[1], ahi));
-  if (U == 3) {
-    sw = sn;
-    products_done();
+  for (int g = 0; g < 4; ++g) {
+    const int part = ((2 * kg + (g >> 1)) ^ (t.l16 >> 1)) * 16 + ((g ^ kg) & 1) * 8;
+    t.at_a[g] = (t.wi * 64 + fragment_row<PAIRS>(t.l16)) * 128 + part;
+    t.at_b[g] = (t.wj * 64 + t.l16) * 128 + part;
   }
 }
 
-// The same for a tile whose rows are all in B's first half.
-template <int U>
-__device__ __forceinline__ void half_step(const BigOperand& a, const BigOperand& b, const Offsets& o, int32_t k,
-                                          int32_t blocks, uint8_t* alo, uint8_t* ahi, uint8_t* bx, uint8_t* next_alo,
-                                          uint8_t* next_bx, i32x8 (&fal)[4], i32x8 (&fah)[4], i32x8 (&fb)[4],
-                                          i32x8 (&fbn)[4], const ScaleSource& ss, ScaleWords& sw, ScaleWords& sn,
-                                          f32x4 (&acc)[8][8]) {
-  meet<12>();
-  quadrant<0, 0, U, true>(fal, fb, sw.a, sw.b, acc, ahi, o.read_a, fah, HalfLoad(a, k + 2, blocks, o.a[0], alo));
-  load_half(b, k + 2, blocks, o.b[0], bx);
-  meet<12>();
-  if (U == 2) load_scales(ss, min(k + 2, blocks - 1) & ~3, sn);
+// Eight bytes of fragment i; the fragments' rows lie in two halves.
+template <bool PAIRS>
+__device__ __forceinline__ i32x2v read_raw(const uint8_t* lo, const uint8_t* hi, int at, int i) {
+  return *reinterpret_cast<const i32x2v*>((i < 4 ? lo : hi) + at + fragment_at<PAIRS>(i & 3));
+}
+
+// Scale byte of this lane's row of fragment j, s the block's bytes (a resource, so
+// that a row costs one register and not an address).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t scales_of(const uint8_t* s) { return row_rsrc(s, 0x7FFFFFFFu); }
+template <bool ROWS>
+__device__ __forceinline__ int scale_a(const WideTile& t, __amdgpu_buffer_rsrc_t s, int j) {
+  return __builtin_amdgcn_raw_buffer_load_b8(s, ROWS ? 0 : min(b_row(t.wi, j, t.l16), t.a.last), 0, 0);
+}
+template <bool ROWS>
+__device__ __forceinline__ int scale_b(const WideTile& t, __amdgpu_buffer_rsrc_t s, int j) {
+  const int32_t row = min(b_row(t.wj, j, t.l16), t.b.last);
+  return __builtin_amdgcn_raw_buffer_load_b8(s, ROWS ? row * t.scale_row : row, 0, 0);
+}
+
+// Block k in LDS buffers [half] of its parity; n_*: the other parity's, where
+// block k + 1 is or arrives.  B's halves are read up to step 19 and A's up to
+// step 26; behind the barriers there the loads of block k + 2 go into them, 32
+// steps (about 4100 cycles of products with J = 8) before they are read.
+template <int J, bool ROWS>
+__device__ __forceinline__ void wide_block(const WideTile& t, WideState& w, int32_t k, int32_t blocks, uint8_t* al,
+                                           uint8_t* ah, uint8_t* bl, uint8_t* bh, uint8_t* nal, uint8_t* nah, uint8_t* nbl,
+                                           uint8_t* nbh, f32x4 (&acc)[8][8]) {
+  constexpr int kScalesA = ROWS ? 1 : 8;
+  const HalfLoad load_al(t.a, k + 2, blocks, t.off_a[0], al), load_ah(t.a, k + 2, blocks, t.off_a[1], ah);
+  const HalfLoad load_bl(t.b, k + 2, blocks, t.off_b[0], bl), load_bh(t.b, k + 2, blocks, t.off_b[1], bh);
+  const int64_t next = min(k + 1, blocks - 1);
+  const __amdgpu_buffer_rsrc_t sa = scales_of(t.scale_a + next * t.pitch_a), sb = scales_of(t.scale_b + next * t.pitch_b);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) fbn[i] = read_fragment<false>(next_bx, o.read_b, i);
-  quadrant<4, 0, U, true>(fah, fb, sw.a, sw.b, acc, next_alo, o.read_a, fal, HalfLoad(a, k + 2, blocks, o.a[1], ahi));
-  if (U == 3) {
-    sw = sn;
+  for (int n = 0; n < 32; ++n) {
+    const int g = n >> 3, i = n & 7;
+    if (n == 20) meet<8>();
+    if (n == 27) meet<J>();
+    if (n == 24) {
+#pragma unroll
+      for (int j = 0; j < J; ++j) w.sb[j] = scale_of(w.nb[j]);
+    }
+    if (n == 31) {
+#pragma unroll
+      for (int j = 0; j < kScalesA; ++j) w.sa[j] = scale_of(w.na[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      product_wide(acc[i][j], w.a[n & 1], w.b[g & 1][j]);
+      if (j == 0) widen_half<0>(w.a[(n + 1) & 1], w.raw_a[(n + 1) & 3], w.sa[(n + 1) & (kScalesA - 1)]);
+      if (j == 1) widen_half<1>(w.a[(n + 1) & 1], w.raw_a[(n + 1) & 3], w.sa[(n + 1) & (kScalesA - 1)]);
+      if (j == 2 && i < J) widen_half<0>(w.b[(g + 1) & 1][i], w.raw_b[n & 3], w.sb[i]);
+      if (j == 3 && i < J) widen_half<1>(w.b[(g + 1) & 1][i], w.raw_b[n & 3], w.sb[i]);
+      if (j == J / 2) {  // behind the last use of the bytes it replaces
+        const int m = n + 5;
+        w.raw_a[m & 3] = m < 32 ? read_raw<ROWS>(al, ah, t.at_a[(m >> 3) & 3], m & 7)
+                                : read_raw<ROWS>(nal, nah, t.at_a[0], m & 7);
+      }
+      if (j == J / 2 + 1 && ((n + 4) & 7) < J) {
+        const int m = n + 4;  // widened at step m for g + 1
+        w.raw_b[m & 3] = m < 24 ? read_raw<false>(bl, bh, t.at_b[((m >> 3) + 1) & 3], m & 7)
+                                : read_raw<false>(nbl, nbh, t.at_b[((m >> 3) + 1) & 3], m & 7);
+      }
+      if (j == J - 2) {
+        if (n >= 2 && n < 2 + kScalesA) w.na[n - 2] = scale_a<ROWS>(t, sa, n - 2);
+        if (n >= 20 && n < 24) load_bl.issue(n - 20);
+        if (n >= 27 && n < 31) load_al.issue(n - 27);
+      }
+      if (j == J - 1) {
+        if (n >= 2 && n < 2 + J) w.nb[n - 2] = scale_b<ROWS>(t, sb, n - 2);
+        if (J == 8 && n >= 20 && n < 24) load_bh.issue(n - 20);
+        if (n >= 27 && n < 31) load_ah.issue(n - 27);
+      }
+    }
+  }
+}
+
+// All blocks of a tile; LDS buffers [block parity][half].
+template <int J, bool ROWS>
+__device__ __forceinline__ void wide_tile(const WideTile& t, int32_t blocks, uint8_t* a00, uint8_t* a01, uint8_t* a10,
+                                          uint8_t* a11, uint8_t* b00, uint8_t* b01, uint8_t* b10, uint8_t* b11,
+                                          f32x4 (&acc)[8][8]) {
+  constexpr int kScalesA = ROWS ? 1 : 8;
+  WideState w;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if (j < kScalesA) w.sa[j] = scale_of(scale_a<ROWS>(t, scales_of(t.scale_a), j));
+    if (j < J) w.sb[j] = scale_of(scale_b<ROWS>(t, scales_of(t.scale_b), j));
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if (j < kScalesA) asm volatile("" : "+v"(w.sa[j]));
+    if (j < J) asm volatile("" : "+v"(w.sb[j]));
+  }
+  load_half(t.b, 0, blocks, t.off_b[0], b00);
+  if (J == 8) load_half(t.b, 0, blocks, t.off_b[1], b01);
+  load_half(t.a, 0, blocks, t.off_a[0], a00);
+  load_half(t.a, 0, blocks, t.off_a[1], a01);
+  load_half(t.b, 1, blocks, t.off_b[0], b10);
+  if (J == 8) load_half(t.b, 1, blocks, t.off_b[1], b11);
+  load_half(t.a, 1, blocks, t.off_a[0], a10);
+  load_half(t.a, 1, blocks, t.off_a[1], a11);
+  meet<8 + J>();
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const i32x2v raw = read_raw<false>(b00, b01, t.at_b[0], j);
+    widen_half<0>(w.b[0][j], raw, w.sb[j]);
+    widen_half<1>(w.b[0][j], raw, w.sb[j]);
+  }
+  const i32x2v raw = read_raw<ROWS>(a00, a01, t.at_a[0], 0);
+  widen_half<0>(w.a[0], raw, w.sa[0]);
+  widen_half<1>(w.a[0], raw, w.sa[0]);
+#pragma unroll
+  for (int m = 0; m < 4; ++m) {
+    w.raw_a[(m + 1) & 3] = read_raw<ROWS>(a00, a01, t.at_a[0], m + 1);
+    w.raw_b[m] = read_raw<false>(b00, b01, t.at_b[1], m);
+  }
+  asm volatile("s_nop 1");
+  for (int32_t k = 0; k < blocks; k += 2) {
+    wide_block<J, ROWS>(t, w, k, blocks, a00, a01, b00, b01, a10, a11, b10, b11, acc);
+    wide_block<J, ROWS>(t, w, k + 1, blocks, a10, a11, b10, b11, a00, a01, b00, b01, acc);
     products_done();
   }
 }
@@ -324,18 +375,15 @@ __device__ __forceinline__ bool usable(const uint8_t* w, const uint8_t* ws) {
 // rows; one tile of 256 columns and up to `unit` rows a workgroup, four waves of
 // 128 x 128 (128 x 64 when the rows fit B's first half).
 //
-// Bound by the matrix units' rate at the clock they leave (about 2.0 GHz), and
-// next to that by the loads into LDS: alone, the products of a block of a full
-// tile take 1.0-1.3 us, its 64 KiB of loads 1.5 us, together 1.55 us.  Larger
-// tiles do not fit the registers.  32768 rows by 6 experts of 4096 x 7168: 730-780
-// us, 2.5-2.6 PFLOP/s; 8192 x 8192 x 8192: 430 us, 2.56 PFLOP/s (a library's plain
-// 8-bit product reaches 2.71-2.78 there).  When the last round of tiles fills at
-// most half of the CUs, two workgroups take the halves of each (32768 rows: 747 ->
-// 740 us; 34000: 800 -> 769; 16500 by 4 experts of 4096 x 1536: 117 -> 109).
-// Measured and not kept: one workgroup a CU that walks the tiles and loads the
-// next one's blocks before it stores (829 us: the hardware's dealing balances
-// better); a barrier a quadrant (853 us against 875, before the loads were
-// spread); all of a half's loads at once (875 us against 807).
+// Bound by the bf16 products at the clock they leave; larger tiles do not fit the
+// registers.  32768 rows by 6 experts of 4096 x 7168: 1237-1256 us, 1.5 PFLOP/s;
+// 8192 x 8192 x 8192: 655 us, 1.7 PFLOP/s (a library's plain bf16 product reaches
+// 1.24 there).  The 8-bit products that do not keep fp32 sums (see above) took 746
+// and 384 us in the same loop.  A tile of at most 128 rows is bound by issue: 192
+// widening instructions and 128 products a block, 1.3 us of which the products are
+// 0.9.  When the last round of tiles fills at most half of the CUs, two workgroups
+// take the halves of each (32768 rows: 1261 -> 1237 us; 34000: 1287 -> 1272; 16500
+// by 4 experts of 4096 x 1536: 174 -> 167).
 __global__ __launch_bounds__(kMmThreads, 1) void expert_gemm_big_kernel(GemmArgs g, int32_t ntile,
                                                                         int32_t unit) {
   __shared__ __align__(16) uint8_t a00[kHalfBytes], a01[kHalfBytes], a10[kHalfBytes], a11[kHalfBytes];
@@ -356,40 +404,39 @@ __global__ __launch_bounds__(kMmThreads, 1) void expert_gemm_big_kernel(GemmArgs
   const uint8_t* ws = g.w_scale[rt.p];
   if (!usable(wp, ws)) return;
   const int32_t n0 = at.n * kBigTile, rows = rt.rows, cols = min(g.N - n0, kBigTile);
-  const BigOperand a{wp + static_cast<int64_t>(n0) * Kp, 128, static_cast<uint32_t>(Kp), cols - 1};
-  const BigOperand b{g.q + rt.row0 * Kp, 128, static_cast<uint32_t>(Kp), rows - 1};
-  const int32_t sblock = min(n0 / 128 + wi, ceil_div(g.N, 128) - 1);
-  const ScaleSource ss{ws + static_cast<int64_t>(sblock) * Ks, g.q_scale + rt.row0 * Ks, Ks, rows - 1};
-  Offsets o;
-  load_offsets<true, 0>(a, o.a[0]);
-  load_offsets<true, 1>(a, o.a[1]);
-  load_offsets<false, 0>(b, o.b[0]);
-  load_offsets<false, 1>(b, o.b[1]);
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int part = ((2 * kg + h) ^ (l16 >> 1)) * 16;
-    o.read_a[h] = (wi * 64 + fragment_row<true>(l16)) * 128 + part;
-    o.read_b[h] = (wj * 64 + fragment_row<false>(l16)) * 128 + part;
-  }
-  ScaleWords sw, sn;
-  load_scales(ss, 0, sw);
-  settle(sw);
+  WideTile t;
+  t.a = BigOperand{wp + static_cast<int64_t>(n0) * Kp, 128, static_cast<uint32_t>(Kp), cols - 1};
+  t.b = BigOperand{g.q + rt.row0 * Kp, 128, static_cast<uint32_t>(Kp), rows - 1};
+  t.scale_a = ws + static_cast<int64_t>(min(n0 / 128 + wi, ceil_div(g.N, 128) - 1)) * Ks;
+  t.scale_b = g.q_scale + rt.row0 * Ks;
+  t.pitch_a = t.pitch_b = 1;
+  t.scale_row = Ks;
+  t.wi = wi;
+  t.wj = wj;
+  t.l16 = l16;
+  load_offsets<true, 0>(t.a, t.off_a[0]);
+  load_offsets<true, 1>(t.a, t.off_a[1]);
+  load_offsets<false, 0>(t.b, t.off_b[0]);
+  load_offsets<false, 1>(t.b, t.off_b[1]);
+  read_offsets<true>(t);
   f32x4 acc[8][8];
 #pragma unroll
   for (int i = 0; i < 8; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  i32x8 fal[4], fah[4], fb0[4], fb1[4];
   // A fragment of rows at a time through the wave's own piece of LDS, so that a
   // store covers 256 consecutive bytes of four rows and need not go by way of the
-  // caches (32768 rows by 4 experts of 4096 x 1536: 218 us; straight from the
-  // registers, 64 bytes of sixteen rows, 235).
+  // caches.
   uint8_t* const stage = wv == 0 ? a00 : wv == 1 ? a01 : wv == 2 ? a10 : a11;
+  uint16_t* const out = g.out + rt.row0 * g.N + n0;
   const auto store = [&](int j0, int j1) {
     meet<0>();  // LDS is free: the last loads (zeros) have arrived, the reads are done
     const int c = wi * 128 + 8 * l16;
 #pragma unroll
     for (int j = j0; j < j1; ++j) {
+      // copied to the other registers here, and not all 256 at the loop's end
+#pragma unroll
+      for (int i = 0; i < 8; ++i) asm volatile("" : "+a"(acc[i][j]));
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         *reinterpret_cast<u32x4*>(stage + l16 * 272 + 64 * i + 16 * kg) =
@@ -401,49 +448,15 @@ __global__ __launch_bounds__(kMmThreads, 1) void expert_gemm_big_kernel(GemmArgs
         const int r = b_row(wj, j, 4 * u + kg);
         const u32x4 y = *reinterpret_cast<const u32x4*>(stage + (4 * u + kg) * 272 + 16 * l16);
         if (r < rows && c < cols)
-          __builtin_nontemporal_store(y, reinterpret_cast<u32x4*>(g.out + (rt.row0 + r) * g.N + n0 + c));
+          __builtin_nontemporal_store(y, reinterpret_cast<u32x4*>(out + static_cast<uint32_t>(r * g.N + c)));
       }
     }
   };
-  load_half(a, 0, blocks, o.a[0], a00);
-  load_half(b, 0, blocks, o.b[0], b00);
   if (rows > 128) {
-    load_half(b, 0, blocks, o.b[1], b01);
-    load_half(a, 0, blocks, o.a[1], a01);
-    load_half(a, 1, blocks, o.a[0], a10);
-    load_half(b, 1, blocks, o.b[1], b11);
-    load_half(b, 1, blocks, o.b[0], b10);
-    load_half(a, 1, blocks, o.a[1], a11);
-    meet<24>();
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      fal[i] = read_fragment<true>(a00, o.read_a, i);
-      fb0[i] = read_fragment<false>(b00, o.read_b, i);
-    }
-    for (int32_t k = 0; k < blocks; k += 4) {
-      big_step<0>(a, b, o, k, blocks, a00, a01, b00, b01, a10, b11, fal, fah, fb0, fb1, ss, sw, sn, acc);
-      big_step<1>(a, b, o, k + 1, blocks, a10, a11, b11, b10, a00, b00, fal, fah, fb1, fb0, ss, sw, sn, acc);
-      big_step<2>(a, b, o, k + 2, blocks, a00, a01, b00, b01, a10, b11, fal, fah, fb0, fb1, ss, sw, sn, acc);
-      big_step<3>(a, b, o, k + 3, blocks, a10, a11, b11, b10, a00, b00, fal, fah, fb1, fb0, ss, sw, sn, acc);
-    }
+    wide_tile<8, true>(t, blocks, a00, a01, a10, a11, b00, b01, b10, b11, acc);
     store(0, 8);
   } else {
-    load_half(a, 0, blocks, o.a[1], a01);
-    load_half(a, 1, blocks, o.a[0], a10);
-    load_half(b, 1, blocks, o.b[0], b10);
-    load_half(a, 1, blocks, o.a[1], a11);
-    meet<16>();
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      fal[i] = read_fragment<true>(a00, o.read_a, i);
-      fb0[i] = read_fragment<false>(b00, o.read_b, i);
-    }
-    for (int32_t k = 0; k < blocks; k += 4) {
-      half_step<0>(a, b, o, k, blocks, a00, a01, b00, a10, b10, fal, fah, fb0, fb1, ss, sw, sn, acc);
-      half_step<1>(a, b, o, k + 1, blocks, a10, a11, b10, a00, b00, fal, fah, fb1, fb0, ss, sw, sn, acc);
-      half_step<2>(a, b, o, k + 2, blocks, a00, a01, b00, a10, b10, fal, fah, fb0, fb1, ss, sw, sn, acc);
-      half_step<3>(a, b, o, k + 3, blocks, a10, a11, b10, a00, b00, fal, fah, fb1, fb0, ss, sw, sn, acc);
-    }
+    wide_tile<4, true>(t, blocks, a00, a01, a10, a11, b00, b01, b10, b11, acc);
     store(0, 4);
   }
 }
@@ -455,24 +468,37 @@ constexpr int kThinWaves = 4;
 constexpr int kThinThreads = 64 * kThinWaves;
 constexpr int kThinRows = 32, kThinCols = 32;
 
-// Fragment of 16 rows: lane's two 16-byte parts kg and kg + 4 of its row, so
+// Fragment of 16 rows: the lane's two 16-byte parts kg and kg + 4 of its row, so
 // that one load covers 64 bytes of each row in order.  Both operands take the
 // same parts, so the products pair the same k.
-__device__ __forceinline__ i32x8 thin_fragment(const uint8_t* row) {
-  return __builtin_shufflevector(*reinterpret_cast<const i32x4*>(row), *reinterpret_cast<const i32x4*>(row + 64), 0, 1, 2, 3,
-                                 4, 5, 6, 7);
+struct ThinFragment {
+  i32x4 part[2];
+};
+
+__device__ __forceinline__ ThinFragment thin_fragment(const uint8_t* row) {
+  return ThinFragment{{*reinterpret_cast<const i32x4*>(row), *reinterpret_cast<const i32x4*>(row + 64)}};
+}
+
+// Bytes 8 * s..8 * s + 7 of the fragment, times their scale, as bf16.
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+__device__ __forceinline__ bf16x8 thin_widen(const ThinFragment& f, int s, float scale) {
+  const uint32_t lo = static_cast<uint32_t>(f.part[s >> 1][2 * (s & 1)]), hi = static_cast<uint32_t>(f.part[s >> 1][2 * (s & 1) + 1]);
+  const bf16x2 v0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false);
+  const bf16x2 v1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true);
+  const bf16x2 v2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false);
+  const bf16x2 v3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true);
+  return bf16x8{v0[0], v0[1], v1[0], v1[1], v2[0], v2[1], v3[0], v3[1]};
 }
 
 // 32 weight rows by 16 or 32 rows.  The four waves split the blocks of 128
 // (wave v takes v, v + 4, ...), every weight byte goes from memory to the
 // registers of the one wave that uses it, the next block's while this one is
 // multiplied, and the waves' sums meet in LDS and are added in wave order.
-// Bound by HBM: 41 rows by 6 experts of 4096 x 7168 (177 MB) take 34-37 us, 4.8-5.2
-// TB/s, the rate of a large copy.  Tiles of 16 rows alone read an expert's weights
-// twice as often: 96 rows 55 us instead of 49, 128 rows of one expert 46 instead of
-// 32.  With 64 columns a tile 36-38 us with four waves, 38 with two or eight; 128
-// columns 43; loads two blocks ahead are slower (fewer waves fit), as are
-// non-temporal loads (46 us).
+// Bound by HBM: 41 rows by 6 experts of 4096 x 7168 (177 MB) take 37 us, 4.8 TB/s.
+// Tiles of 16 rows alone read an expert's weights twice as often: 96 rows 61 us
+// instead of 52, 128 rows of one expert 43 instead of 31.  With 64 columns a tile 38
+// us, 53 and 25, but one expert's 16 or 32 rows 20 and 25 instead of 14; with 16
+// columns 43, 64, 44, and 11.5 and 15.
 constexpr int kThinFrags = kThinCols / 16;
 struct ThinSums {
   float v[kThinWaves][kThinRows][kThinCols + 4];
@@ -500,7 +526,7 @@ __device__ __forceinline__ void thin_tile(const GemmArgs& g, const RowTile& rt, 
   for (int i = 0; i < FN; ++i)
 #pragma unroll
     for (int j = 0; j < FR; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  i32x8 fa[FN], fb[FR];
+  ThinFragment fa[FN], fb[FR];
   int xa, xb[FR];
   const auto load = [&](int32_t block) {
     const int32_t b = min(block, blocks - 1);
@@ -515,10 +541,17 @@ __device__ __forceinline__ void thin_tile(const GemmArgs& g, const RowTile& rt, 
   load(wv);
   for (int32_t b = wv; b < blocks; b += kThinWaves) {
 #pragma unroll
-    for (int i = 0; i < FN; ++i)
+    for (int s = 0; s < 4; ++s) {
+      bf16x8 wa[FN], wb[FR];
 #pragma unroll
-      for (int j = 0; j < FR; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fa[i], fb[j], acc[i][j], 0, 0, 0, xa, 0, xb[j]);
+      for (int i = 0; i < FN; ++i) wa[i] = thin_widen(fa[i], s, scale_of(xa));
+#pragma unroll
+      for (int j = 0; j < FR; ++j) wb[j] = thin_widen(fb[j], s, scale_of(xb[j]));
+#pragma unroll
+      for (int i = 0; i < FN; ++i)
+#pragma unroll
+        for (int j = 0; j < FR; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wa[i], wb[j], acc[i][j], 0, 0, 0);
+    }
     load(b + kThinWaves);
   }
 #pragma unroll
@@ -563,159 +596,8 @@ __global__ __launch_bounds__(kThinThreads) void expert_gemm_thin_kernel(GemmArgs
 }
 
 // ------------------------------------------------------------------------
-// The weight gradients' 256 x 256 tile
+// The weight gradients
 // ------------------------------------------------------------------------
-typedef int i32x2v __attribute__((ext_vector_type(2)));
-
-// acc += A B of one 16 x 16 x 32 in bf16, in place (see product); nothing that
-// it reads is written by the two vector instructions before it.
-__device__ __forceinline__ void product_wide(f32x4& acc, const i32x4& a, const i32x4& b) {
-  asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
-}
-
-// Values 4 * HALF..4 * HALF + 3 of eight e4m3 bytes, times their scale, as bf16.
-template <int HALF>
-__device__ __forceinline__ void widen_half(i32x4& y, const i32x2v& raw, float scale) {
-  int lo, hi;
-  asm volatile("v_cvt_scalef32_pk_bf16_fp8 %0, %1, %2" : "=v"(lo) : "v"(raw[HALF]), "v"(scale));
-  asm volatile("v_cvt_scalef32_pk_bf16_fp8 %0, %1, %2 op_sel:[1,0,0]" : "=v"(hi) : "v"(raw[HALF]), "v"(scale));
-  y[2 * HALF] = lo;
-  y[2 * HALF + 1] = hi;
-}
-
-// A block of 128 is 32 steps n = 8 g + i: A's fragment i by B's J (eight, or the
-// four of its first half), over the g-th eight of each lane's 32 values.  During
-// step n the fragment of A for step n + 1 and fragment i of B for the next g are
-// widened, an instruction or two behind each product, from bytes read from LDS
-// four steps before.
-struct WideState {
-  i32x4 a[2];     // A's fragment of this step and of the next
-  i32x4 b[2][8];  // B's of this g and of the next
-  i32x2v raw_a[4], raw_b[4];
-  float sa[8], sb[8];  // scales of the block being widened
-  int na[8], nb[8];    // scale bytes of the next one
-};
-
-struct WideTile {
-  BigOperand a, b;
-  const uint8_t *scale_a, *scale_b;  // scale bytes of the tile's rows, block 0
-  int32_t pitch_a, pitch_b;          // scale bytes a block
-  int32_t wi, wj, l16;
-  uint32_t off_a[2][4], off_b[2][4];
-  int at_a[4], at_b[4];              // LDS offset of this lane's eight bytes g, in a half
-};
-
-// Eight bytes of fragment i; the fragments' rows lie in two halves.
-__device__ __forceinline__ i32x2v read_raw(const uint8_t* lo, const uint8_t* hi, int at, int i) {
-  return *reinterpret_cast<const i32x2v*>((i < 4 ? lo : hi) + at + fragment_at<false>(i & 3));
-}
-
-__device__ __forceinline__ int scale_byte(const uint8_t* s, int32_t row, int32_t last) { return s[min(row, last)]; }
-
-// Block k in LDS buffers [half] of its parity; n_*: the other parity's, where
-// block k + 1 is or arrives.  B's halves are read up to step 19 and A's up to
-// step 26; behind the barriers there the loads of block k + 2 go into them, 32
-// steps (about 4100 cycles of products with J = 8) before they are read.
-template <int J>
-__device__ __forceinline__ void wide_block(const WideTile& t, WideState& w, int32_t k, int32_t blocks, uint8_t* al,
-                                           uint8_t* ah, uint8_t* bl, uint8_t* bh, uint8_t* nal, uint8_t* nah, uint8_t* nbl,
-                                           uint8_t* nbh, f32x4 (&acc)[8][8]) {
-  const HalfLoad load_al(t.a, k + 2, blocks, t.off_a[0], al), load_ah(t.a, k + 2, blocks, t.off_a[1], ah);
-  const HalfLoad load_bl(t.b, k + 2, blocks, t.off_b[0], bl), load_bh(t.b, k + 2, blocks, t.off_b[1], bh);
-  const int64_t next = min(k + 1, blocks - 1);
-  const uint8_t* sa = t.scale_a + next * t.pitch_a;
-  const uint8_t* sb = t.scale_b + next * t.pitch_b;
-#pragma unroll
-  for (int n = 0; n < 32; ++n) {
-    const int g = n >> 3, i = n & 7;
-    if (n == 20) meet<8>();
-    if (n == 27) meet<J>();
-    if (n == 24) {
-#pragma unroll
-      for (int j = 0; j < J; ++j) w.sb[j] = scale_of(w.nb[j]);
-    }
-    if (n == 31) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) w.sa[j] = scale_of(w.na[j]);
-    }
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      product_wide(acc[i][j], w.a[n & 1], w.b[g & 1][j]);
-      if (j == 0) widen_half<0>(w.a[(n + 1) & 1], w.raw_a[(n + 1) & 3], w.sa[(n + 1) & 7]);
-      if (j == 1) widen_half<1>(w.a[(n + 1) & 1], w.raw_a[(n + 1) & 3], w.sa[(n + 1) & 7]);
-      if (j == 2 && i < J) widen_half<0>(w.b[(g + 1) & 1][i], w.raw_b[n & 3], w.sb[i]);
-      if (j == 3 && i < J) widen_half<1>(w.b[(g + 1) & 1][i], w.raw_b[n & 3], w.sb[i]);
-      if (j == J / 2) {  // behind the last use of the bytes it replaces
-        const int m = n + 5;
-        w.raw_a[m & 3] = m < 32 ? read_raw(al, ah, t.at_a[(m >> 3) & 3], m & 7)
-                                : read_raw(nal, nah, t.at_a[0], m & 7);
-      }
-      if (j == J / 2 + 1 && ((n + 4) & 7) < J) {
-        const int m = n + 4;  // widened at step m for g + 1
-        w.raw_b[m & 3] = m < 24 ? read_raw(bl, bh, t.at_b[((m >> 3) + 1) & 3], m & 7)
-                                : read_raw(nbl, nbh, t.at_b[((m >> 3) + 1) & 3], m & 7);
-      }
-      if (j == J - 2) {
-        if (n >= 2 && n < 10) w.na[n - 2] = scale_byte(sa, b_row(t.wi, n - 2, t.l16), t.a.last);
-        if (n >= 20 && n < 24) load_bl.issue(n - 20);
-        if (n >= 27 && n < 31) load_al.issue(n - 27);
-      }
-      if (j == J - 1) {
-        if (n >= 2 && n < 2 + J) w.nb[n - 2] = scale_byte(sb, b_row(t.wj, n - 2, t.l16), t.b.last);
-        if (J == 8 && n >= 20 && n < 24) load_bh.issue(n - 20);
-        if (n >= 27 && n < 31) load_ah.issue(n - 27);
-      }
-    }
-  }
-}
-
-// All blocks of a tile; LDS buffers [block parity][half].
-template <int J>
-__device__ __forceinline__ void wide_tile(const WideTile& t, int32_t blocks, uint8_t* a00, uint8_t* a01, uint8_t* a10,
-                                          uint8_t* a11, uint8_t* b00, uint8_t* b01, uint8_t* b10, uint8_t* b11,
-                                          f32x4 (&acc)[8][8]) {
-  WideState w;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    w.sa[j] = scale_of(scale_byte(t.scale_a, b_row(t.wi, j, t.l16), t.a.last));
-    if (j < J) w.sb[j] = scale_of(scale_byte(t.scale_b, b_row(t.wj, j, t.l16), t.b.last));
-  }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    asm volatile("" : "+v"(w.sa[j]));
-    if (j < J) asm volatile("" : "+v"(w.sb[j]));
-  }
-  load_half(t.b, 0, blocks, t.off_b[0], b00);
-  if (J == 8) load_half(t.b, 0, blocks, t.off_b[1], b01);
-  load_half(t.a, 0, blocks, t.off_a[0], a00);
-  load_half(t.a, 0, blocks, t.off_a[1], a01);
-  load_half(t.b, 1, blocks, t.off_b[0], b10);
-  if (J == 8) load_half(t.b, 1, blocks, t.off_b[1], b11);
-  load_half(t.a, 1, blocks, t.off_a[0], a10);
-  load_half(t.a, 1, blocks, t.off_a[1], a11);
-  meet<8 + J>();
-#pragma unroll
-  for (int j = 0; j < J; ++j) {
-    const i32x2v raw = read_raw(b00, b01, t.at_b[0], j);
-    widen_half<0>(w.b[0][j], raw, w.sb[j]);
-    widen_half<1>(w.b[0][j], raw, w.sb[j]);
-  }
-  const i32x2v raw = read_raw(a00, a01, t.at_a[0], 0);
-  widen_half<0>(w.a[0], raw, w.sa[0]);
-  widen_half<1>(w.a[0], raw, w.sa[0]);
-#pragma unroll
-  for (int m = 0; m < 4; ++m) {
-    w.raw_a[(m + 1) & 3] = read_raw(a00, a01, t.at_a[0], m + 1);
-    w.raw_b[m] = read_raw(b00, b01, t.at_b[1], m);
-  }
-  asm volatile("s_nop 1");
-  for (int32_t k = 0; k < blocks; k += 2) {
-    wide_block<J>(t, w, k, blocks, a00, a01, b00, b01, a10, a11, b10, b11, acc);
-    wide_block<J>(t, w, k + 1, blocks, a10, a11, b10, b11, a00, a01, b00, b01, acc);
-    products_done();
-  }
-}
-
 // Four consecutive values of a gradient; vec: its address allows 16-byte accesses.
 __device__ __forceinline__ void put_gradient(float* d, f32x4 y, bool accumulate, bool vec) {
   if (vec) {
@@ -797,18 +679,11 @@ __global__ __launch_bounds__(kMmThreads, 1) void expert_wgrad_big_kernel(
     load_offsets<false, 1>(t.a, t.off_a[1]);
     load_offsets<false, 0>(t.b, t.off_b[0]);
     load_offsets<false, 1>(t.b, t.off_b[1]);
-    // odd lanes of sixteen take the two eights of a part the other way round, so
-    // that 32 lanes reading eight bytes meet all banks once
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const int part = ((2 * kg + (g >> 1)) ^ (l16 >> 1)) * 16 + ((g ^ kg) & 1) * 8;
-      t.at_a[g] = (wi * 64 + l16) * 128 + part;
-      t.at_b[g] = (wj * 64 + l16) * 128 + part;
-    }
+    read_offsets<false>(t);
     if (rows > 128)
-      wide_tile<8>(t, blocks, a00, a01, a10, a11, b00, b01, b10, b11, acc);
+      wide_tile<8, false>(t, blocks, a00, a01, a10, a11, b00, b01, b10, b11, acc);
     else
-      wide_tile<4>(t, blocks, a00, a01, a10, a11, b00, b01, b10, b11, acc);
+      wide_tile<4, false>(t, blocks, a00, a01, a10, a11, b00, b01, b10, b11, acc);
   }
   const bool vec = (reinterpret_cast<uintptr_t>(out) & 15) == 0;
   // a fragment of rows at a time through the wave's own piece of LDS, so that a
@@ -841,32 +716,32 @@ hipError_t launch_expert_gemm(const int32_t* off, int32_t ne, const uint8_t* q, 
   if (ne == 0 || cap == 0) return hipSuccess;
   const GemmArgs g{off, ne, q, q_scale, K, w, w_scale, N, out, cap};
   const int32_t nbig = ceil_div(N, kBigTile);
-  // Few rows.  Thin tiles take each row tile's weights from memory at 5.2 TB/s,
-  // cap / 32 + ne / 2 or so row tiles; big ones 0.8 us a block of 128 of K and
+  // Few rows.  Thin tiles take each row tile's weights from memory at 4.8 TB/s,
+  // cap / 32 + ne / 2 or so row tiles; big ones 1.3 us a block of 128 of K and
   // more the more of them share the memory, whatever the rows.  Both grow with
-  // K alike, which leaves a bound on rows and N; and up to four rows an expert
+  // K alike, which leaves a bound on rows and N; and up to eight rows an expert
   // nearly every thin tile is its expert's only one.  Thin / big, us: 6 experts of
-  // 4096 x 7168 at 4, 16, 24, 33 rows an expert 34/53, 49/57, 60/58, 72/59; 24 of
-  // 2048 x 5120 at 4, 8, 12: 51/51, 60/52, 68/53; 32 of 7168 x 2048 at 4, 8: 85/87,
-  // 101/91; 4 of 1536 x 5120 at 16, 32, 70, 100: 15/31, 21/31, 30/32, 35/33; one of
-  // 4096 x 7168 at 16, 64, 128, 200: 14/40, 18/41, 32/41, 59/41; 8 of 1024 x 1024 at
-  // 32, 55, 100: 8.9/11.1, 11.7/11.4, 14.7/11.5; 2 of 7168 x 2048 at 16, 32, 64:
-  // 12/16, 16/16, 26/17.
-  if (cap <= 4 * static_cast<int64_t>(ne) || (cap + 8 * static_cast<int64_t>(ne)) * N <= 600000) {
+  // 4096 x 7168 at 4, 16, 24, 33 rows an expert 34/81, 54/82, 65/82, 80/82; 24 of
+  // 2048 x 5120 at 4, 8, 12, 16: 55/70, 67/72, 77/73, 84/74; 32 of 7168 x 2048 at 4,
+  // 8: 83/111, 98/115; 4 of 1536 x 5120 at 16, 32, 70, 100: 14/55, 21/55, 29/55,
+  // 34/55; one of 4096 x 7168 at 16, 64, 128, 200: 14/73, 19/74, 33/74, 59/74; 8 of
+  // 1024 x 1024 at 32, 55, 100: 8.9/16, 10/16, 13/17; 2 of 7168 x 2048 at 16, 32,
+  // 64: 12/26, 15/26, 25/26.
+  if (cap <= 8 * static_cast<int64_t>(ne) || (cap + 8 * static_cast<int64_t>(ne)) * N <= 1000000) {
     const int32_t ntile = ceil_div(N, kThinCols);
     // 32 rows a tile, or 16 where that makes too few tiles to keep the memory
-    // busy (32 rows of one expert of 4096 x 7168, 128 or 256 tiles: 18.7 and 14.5
-    // us; 64 rows, 256 or 512: 18.5 and 24.3)
+    // busy (32 rows of one expert of 4096 x 7168, 128 or 256 tiles: 18.0 and 14.3
+    // us; 64 rows, 256 or 512: 18.4 and 23.4)
     const int32_t unit = (cap / kThinRows + ne / 2) * ntile < 192 ? 16 : kThinRows;
     const int64_t tiles = (cap / unit + ne) * ntile;
     hipLaunchKernelGGL(expert_gemm_thin_kernel, dim3(mm_grid(tiles)), dim3(kThinThreads), 0, st, g, ntile, unit);
     return hipGetLastError();
   }
   // Rows a tile, 256 or 128: a tile of 128 takes about 11/15 of the time of one of
-  // 256 (49 and 66 us a round at K = 5120), so what counts is the rounds of 256
+  // 256 (77 and 101 us a round at K = 5120), so what counts is the rounds of 256
   // workgroups; an expert's last tile is half full on average.  64 rows for each of
-  // 24 experts: 59 us in tiles of 128, 66 in tiles of 256; 200: 99 and 117; 500
-  // for each of 6 experts of 4096 x 7168: 122 and 91; 5461: 1010 and 799.
+  // 24 experts: 78 us in tiles of 128, 101 in tiles of 256; 200: 135 and 157; 500
+  // for each of 6 experts of 4096 x 7168: 182 and 149; 5461: 1483 and 1257.
   const auto rounds = [&](int32_t u) { return ((cap / u + ne / 2 + 1) * nbig + 255) / 256; };
   const int32_t unit = 11 * rounds(128) < 15 * rounds(256) ? 128 : 256;
   const int64_t tiles = (cap / unit + ne) * nbig + (unit == kBigTile ? kComputeUnits / 2 : 0);
