@@ -48,7 +48,10 @@
  *
  * Segments.  plan, p_begin and p_end name a range of physical experts as in
  * ultraep_permute; the rows of the range are counted from its first one, and
- * rows at or beyond capacity_rows are not there for any of these calls.
+ * rows at or beyond capacity_rows are not there for any of these calls.  Without
+ * rows (capacity_rows = 0) or experts (p_begin = p_end, n = 0) nothing is read or
+ * written, but for the weight gradients of experts without rows, and a buffer that
+ * so has no elements may be NULL, as hidden may with hidden_rows = 0.
  */
 #ifndef ULTRAEP_EXPERTS_H
 #define ULTRAEP_EXPERTS_H

@@ -32,6 +32,10 @@ const int32_t* segment(const ultraep_ctx* ctx, const void* plan, int32_t p_begin
 
 bool half_given(const void* a, const void* b) { return (a == nullptr) != (b == nullptr); }
 
+// No rows, or no experts to have any: nothing is read or written, and the
+// buffers, having no elements, need no address.
+bool idle(int64_t rows, int32_t p_begin, int32_t p_end) { return rows == 0 || p_begin == p_end; }
+
 }  // namespace
 
 extern "C" {
@@ -41,7 +45,8 @@ int ultraep_permute_quant(const ultraep_ctx* ctx, const void* plan, const int32_
                           int32_t p_end, uint8_t* q, uint8_t* q_scale, uint8_t* qt,
                           uint8_t* qt_scale, int64_t capacity_rows, int64_t capacity_blocks,
                           void* stream) {
-  if (!ctx || !plan || !hidden || half_given(q, q_scale) || half_given(qt, qt_scale) || (!q && !qt))
+  if (!ctx || !plan || (!hidden && hidden_rows > 0)) return ULTRAEP_EINVAL;
+  if (!idle(capacity_rows, p_begin, p_end) && (half_given(q, q_scale) || half_given(qt, qt_scale) || (!q && !qt)))
     return ULTRAEP_EINVAL;
   if (H <= 0 || hidden_rows < 0 || capacity_rows < 0 || bad_range(ctx, p_begin, p_end)) return ULTRAEP_EINVAL;
   if (inv && (k < 1 || k > ULTRAEP_MAX_TOPK)) return ULTRAEP_EINVAL;
@@ -58,7 +63,7 @@ int ultraep_weight_quant(const ultraep_ctx* ctx, const uint16_t* const* weights,
                          int32_t N, int32_t K, uint8_t* q, uint8_t* q_scale, uint8_t* qt,
                          uint8_t* qt_scale, void* stream) {
   if (!ctx || n < 0 || N <= 0 || K <= 0 || (n > 0 && !weights)) return ULTRAEP_EINVAL;
-  if (half_given(q, q_scale) || half_given(qt, qt_scale) || (!q && !qt)) return ULTRAEP_EINVAL;
+  if (n > 0 && (half_given(q, q_scale) || half_given(qt, qt_scale) || (!q && !qt))) return ULTRAEP_EINVAL;
   if (N % 8 != 0 || K % 8 != 0 || N > kMaxWidth || K > kMaxWidth || n > ULTRAEP_MAX_EXPERTS ||
       !aligned(weights, 8) || !aligned(q, 16) || !aligned(qt, 16) || !aligned(q_scale, 4) ||
       !aligned(qt_scale, 4))
@@ -71,7 +76,8 @@ int ultraep_expert_gemm(const ultraep_ctx* ctx, const void* plan, const uint8_t*
                         const uint8_t* q_scale, int32_t K, const uint8_t* const* w,
                         const uint8_t* const* w_scale, int32_t N, int32_t p_begin, int32_t p_end,
                         uint16_t* out, int64_t capacity_rows, void* stream) {
-  if (!ctx || !plan || !q || !q_scale || !w || !w_scale || !out) return ULTRAEP_EINVAL;
+  if (!ctx || !plan) return ULTRAEP_EINVAL;
+  if (!idle(capacity_rows, p_begin, p_end) && (!q || !q_scale || !w || !w_scale || !out)) return ULTRAEP_EINVAL;
   if (N <= 0 || K <= 0 || capacity_rows < 0 || bad_range(ctx, p_begin, p_end)) return ULTRAEP_EINVAL;
   if (N % 8 != 0 || N > kMaxWidth || K > kMaxWidth || capacity_rows >= kMaxRows || !aligned(plan, 4) ||
       !aligned(q, 16) || !aligned(q_scale, 4) || !aligned(w, 8) || !aligned(w_scale, 8) || !aligned(out, 16) ||
@@ -87,7 +93,8 @@ int ultraep_expert_wgrad(const ultraep_ctx* ctx, const void* plan, const uint8_t
                          const uint8_t* xt_scale, int32_t K, int32_t p_begin, int32_t p_end,
                          int64_t capacity_rows, float* const* grads, int32_t accumulate,
                          void* stream) {
-  if (!ctx || !plan || !dyt || !dyt_scale || !xt || !xt_scale || !grads) return ULTRAEP_EINVAL;
+  if (!ctx || !plan) return ULTRAEP_EINVAL;
+  if (p_begin != p_end && (!dyt || !dyt_scale || !xt || !xt_scale || !grads)) return ULTRAEP_EINVAL;
   if (N <= 0 || K <= 0 || capacity_rows < 0 || bad_range(ctx, p_begin, p_end)) return ULTRAEP_EINVAL;
   if (accumulate != 0 && accumulate != 1) return ULTRAEP_EINVAL;
   if (N % 8 != 0 || K % 8 != 0 || N > kMaxWidth || K > kMaxWidth || capacity_rows >= kMaxRows ||
