@@ -124,8 +124,9 @@ def _stream(stream) -> Optional[int]:
     if stream is not None:
         return int(stream) if isinstance(stream, int) else stream.cuda_stream
     import torch
-    # the current stream's handle without building a Stream object (2.7 us of a 5 us call)
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    # the current stream's handle without building a Stream object (2.7 us of a 5 us call); not a public call
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
 
 
 def _ptr(t) -> Optional[int]:
