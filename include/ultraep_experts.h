@@ -118,6 +118,8 @@ int ultraep_weight_quant(const ultraep_ctx* ctx, const uint16_t* const* weights,
  *      misaligned entry are left as they are; entries of experts without rows
  *      are not looked at.
  * Out: out [capacity_rows][N] bf16; rows without an expert are left as they are.
+ * The kernel is chosen by capacity_rows: where few rows come, a capacity near
+ * them is faster (41 rows by 6 experts of 4096 x 7168: 37 us, 81 from 656 up).
  * With the gradient rows for q (K = the forward's N) and the transposed weights
  * this is the gradient of the forward's rows.
  * Errors: EINVAL (null pointers, N <= 0, K <= 0, bad range, capacity_rows < 0);

@@ -35,8 +35,9 @@ __device__ __forceinline__ int64_t source_row(const RowSource& s, int32_t seg0, 
 
 // Rows form alone: one wave per (row, 512 columns), 16 lanes a block, so a
 // block's maximum is four DPP steps and its four scale bytes one store.  Bound by
-// HBM: 32771 rows of 7168 gathered and quantised, 706 MB, 146 us (4.8 TB/s);
-// ordinary instead of non-temporal stores 151.
+// HBM: 32771 rows of 7168 gathered and quantised, 706 MB, 145 us (4.9 TB/s;
+// 20700 distinct tokens, but the counters show every row read); ordinary instead of
+// non-temporal stores 151.
 __global__ __launch_bounds__(kQuantThreads) void quant_rows_kernel(
     const int32_t* __restrict__ off, int32_t ne, RowSource in, int32_t H, uint8_t* __restrict__ q,
     uint8_t* __restrict__ scale, int64_t cap) {

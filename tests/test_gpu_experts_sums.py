@@ -73,3 +73,15 @@ def test_scale_bytes_behind_the_last_block_are_not_used(loads, N):
     qs[:, 3:], ws[:, :, 3:] = 255, 255
     got = run_gemm(seg, q, qs, w, ws, N, K)
     assert np.array_equal(zero(got[:seg.rows]), zero(want))
+
+
+@pytest.mark.parametrize("rows_at,weights_at", [(1, 230), (245, 20)])
+@pytest.mark.parametrize("loads,N,K", SHAPES[:4])
+def test_scales_at_the_ends_of_their_range(loads, N, K, rows_at, weights_at):
+    """Values of 2^-126 to 2^120: still bf16 numbers of the normal range, so the whole numbers' results stay exact."""
+    rng = np.random.default_rng([N, K, rows_at])
+    seg, q, qs, w, ws = operands(rng, loads, N, K, whole=True)
+    qs[:], ws[:] = qs - 126 + rows_at, ws - 126 + weights_at
+    got = run_gemm(seg, q, qs, w, ws, N, K)
+    want, _ = to_bf16(X.expert_gemm(*gemm_values(seg, q, qs, w, ws), seg.off) + 0.0)
+    assert np.array_equal(zero(got[:seg.rows]), zero(want))
