@@ -14,7 +14,9 @@ Names follow the C ABI: ``ultraep_create``, ``ultraep_balance``,
 ``ultraep_weight_sync``, ``ultraep_fold_grads``; and of the experts' own steps
 (``include/ultraep_experts.h``) ``ultraep_permute_quant``,
 ``ultraep_weight_quant``, ``ultraep_expert_gemm``, ``ultraep_expert_wgrad``,
-``ultraep_grad_sumsq``, ``ultraep_grad_clip``.
+``ultraep_grad_sumsq``, ``ultraep_grad_clip``; and of the steps around them
+(``include/ultraep_layer.h``) ``ultraep_route``, ``ultraep_residual_norm``,
+``ultraep_glu_quant`` and each with ``_backward``.
 """
 from __future__ import annotations
 
@@ -94,6 +96,19 @@ _EXPERT_SIGNATURES = {
     "ultraep_grad_sumsq": (_I32, [_P, _P, _P, _I32, _I32, _P, _I32, _P, _SZ, _P]),
     "ultraep_grad_clip": (_I32, [_P, _P, _P, _I32, _I32, _P, ctypes.c_double, _P, _P, _P]),
 }
+# include/ultraep_layer.h
+_LAYER_SIGNATURES = {
+    "ultraep_route": (_I32, [_P, _P, _I32, _I64, _I32, _I32, _P, _I32, _I32, _I32, _I32, ctypes.c_float, _P, _P, _P]),
+    "ultraep_route_backward": (_I32, [_P, _P, _I32, _I64, _I32, _I32, _I32, ctypes.c_float, _P, _P, _P, _P]),
+    "ultraep_residual_norm": (_I32, [_P, _P, _P, _I32, _P, _I32, ctypes.c_float, _I64, _I32, _P, _P, _P, _P, _P, _P]),
+    "ultraep_residual_norm_workspace_bytes": (_I32, [_I64, _I32, ctypes.POINTER(_SZ)]),
+    "ultraep_residual_norm_backward": (_I32, [_P, _P, _P, _I32, _P, _I32, _P, _P, _I64, _I32, _P, _P, _P, _I32, _P, _SZ, _P]),
+    "ultraep_glu_quant": (_I32, [_P, _P, _P, _I32, _I32, _I32, _I32, _P, _P, _P, _P, _I64, _I64, _P]),
+    "ultraep_glu_quant_backward": (_I32, [_P, _P, _P, _P, _I32, _I32, _I32, _I32, _P, _P, _P, _P, _I64, _I64, _P]),
+}
+ROUTE_SOFTMAX, ROUTE_SIGMOID = 0, 1
+GLU_SILU, GLU_GELU = 0, 1
+MAX_ROUTE_GROUPS, MAX_NORM_WIDTH = 64, 32768
 QUANT_BLOCK = 128
 MAX_GRAD_TENSORS = 4096
 GRAD_WORKSPACE_BYTES = 16384
@@ -107,7 +122,7 @@ def lib() -> ctypes.CDLL:
             raise RuntimeError(f"{LIB_PATH} is missing: build it with `python -c 'import "
                                "__graft_entry__ as g; g.build()'` (needs hipcc for gfx950)")
         handle = ctypes.CDLL(LIB_PATH)
-        for name, (res, args) in {**_SIGNATURES, **_EXPERT_SIGNATURES}.items():
+        for name, (res, args) in {**_SIGNATURES, **_EXPERT_SIGNATURES, **_LAYER_SIGNATURES}.items():
             fn = getattr(handle, name)
             fn.restype = res
             fn.argtypes = args
@@ -301,16 +316,16 @@ def pointer_table(tensors, device="cuda"):
     return torch.tensor([0 if t is None else t.data_ptr() for t in tensors], dtype=torch.int64).to(device)
 
 
-_BYTES = _HALVES = _LONGS = _INTS = _device = None
+_BYTES = _HALVES = _LONGS = _INTS = _FLOATS = _device = None
 
 
 def _types():
     """The types a call's buffers may have, and the current device's index, found once torch is in use."""
-    global _BYTES, _HALVES, _LONGS, _INTS, _device
+    global _BYTES, _HALVES, _LONGS, _INTS, _FLOATS, _device
     import torch
     _BYTES = (torch.uint8, torch.float8_e4m3fn)
     _HALVES = (torch.bfloat16, torch.int16, torch.uint16)
-    _LONGS, _INTS = (torch.int64,), (torch.int32,)
+    _LONGS, _INTS, _FLOATS = (torch.int64,), (torch.int32,), (torch.float32,)
     _device = lambda: torch.cuda.current_device() if torch.cuda.is_initialized() else None  # noqa: E731
 
 
@@ -450,6 +465,154 @@ def ultraep_grad_clip(ctx: Context, tensors, numels, n: int, dtype, sumsq, max_n
           and (out is None or (_is(out, dev, (torch.int64,), None) and out.shape[0] >= n)))
     st = lib().ultraep_grad_clip(ctx.handle, _ptr(tensors), _ptr(numels), n, code, _ptr(sumsq), float(max_norm),
                                  _ptr(norm), _ptr(out), _stream(stream))
+    _check(fn, st)
+
+
+# The steps around the experts, with the same checks.
+def _type_code(fn: str, t) -> int:
+    """The code of a buffer's type, fp32 or bf16."""
+    import torch
+    _need(fn, t is not None and (t.dtype is torch.float32 or t.dtype is torch.bfloat16))
+    return int(t.dtype is torch.bfloat16)
+
+
+def _route_checks(fn: str, ctx, dev, logits, k: int, topk_idx, w) -> tuple:
+    """(tokens, type code) of a routing call."""
+    code = _type_code(fn, logits)
+    _need(fn, _is(logits, dev, (logits.dtype,), None, ctx.E))
+    n = logits.shape[0]
+    _need(fn, _is(topk_idx, dev, _INTS, n, k) and _is(w, dev, _FLOATS, n, k))
+    return n, code
+
+
+def ultraep_route(ctx: Context, logits, k: int, topk_idx, topk_w, score: int = ROUTE_SOFTMAX, bias=None, groups: int = 1,
+                  topk_groups: int = 1, group_top: int = 1, renormalize: bool = True, scale: float = 1.0,
+                  stream=None) -> None:
+    """The k experts of every token and their weights.
+
+    logits fp32 or bf16 [tokens, E], bias fp32 [E] (it moves the choice, not the weights); topk_idx int32
+    [tokens, k] (-1 where no expert is left), topk_w fp32 [tokens, k]."""
+    fn = "ultraep_route"
+    dev = _here()
+    n, code = _route_checks(fn, ctx, dev, logits, k, topk_idx, topk_w)
+    _need(fn, bias is None or _is(bias, dev, _FLOATS, ctx.E))
+    st = lib().ultraep_route(ctx.handle, _ptr(logits), code, n, k, score, _ptr(bias), groups, topk_groups, group_top,
+                             int(renormalize), scale, _ptr(topk_idx), _ptr(topk_w), _stream(stream))
+    _check(fn, st)
+
+
+def ultraep_route_backward(ctx: Context, logits, k: int, topk_idx, grad_topk_w, grad_logits, score: int = ROUTE_SOFTMAX,
+                           renormalize: bool = True, scale: float = 1.0, stream=None) -> None:
+    """grad_logits [tokens, E] (the logits' type) from the gradients of ultraep_route's weights."""
+    fn = "ultraep_route_backward"
+    dev = _here()
+    n, code = _route_checks(fn, ctx, dev, logits, k, topk_idx, grad_topk_w)
+    _need(fn, _is(grad_logits, dev, (logits.dtype,), n, ctx.E))
+    st = lib().ultraep_route_backward(ctx.handle, _ptr(logits), code, n, k, score, int(renormalize), scale, _ptr(topk_idx),
+                                      _ptr(grad_topk_w), _ptr(grad_logits), _stream(stream))
+    _check(fn, st)
+
+
+def ultraep_residual_norm(ctx: Context, x, weight, eps: float, residual=None, h=None, y=None, q=None, q_scale=None,
+                          rstd=None, stream=None) -> None:
+    """h = residual + x, y = h * rstd * weight with rstd = 1 / sqrt(mean(h^2) + eps).
+
+    x bf16 [rows, H]; residual and h [rows, H] fp32 or bf16 (h may be the residual); weight [H] fp32 or bf16;
+    y bf16 [rows, H]; q [rows, quant_pitch(H)] with q_scale [rows, quant_scale_pitch(H)] the rows form of y;
+    rstd fp32 [rows].  Outputs that are not wanted are None."""
+    fn = "ultraep_residual_norm"
+    dev = _here()
+    _need(fn, x is not None and x.dim() == 2 and (q is None) == (q_scale is None))
+    n, H = x.shape
+    w_code, r_code = _type_code(fn, weight), 1 if residual is None else _type_code(fn, residual)
+    _need(fn, _is(x, dev, _HALVES, n, H) and _is(weight, dev, (weight.dtype,), H)
+          and (residual is None or _is(residual, dev, (residual.dtype,), n, H))
+          and (h is None or (residual is not None and _is(h, dev, (residual.dtype,), n, H)))
+          and (y is None or _is(y, dev, _HALVES, n, H))
+          and (q is None or (_is(q, dev, _BYTES, n, quant_pitch(H)) and _is(q_scale, dev, _BYTES, n, quant_scale_pitch(H))))
+          and (rstd is None or _is(rstd, dev, _FLOATS, n)))
+    st = lib().ultraep_residual_norm(ctx.handle, _ptr(x), _ptr(residual), r_code, _ptr(weight), w_code, eps, n, H, _ptr(h),
+                                     _ptr(y), _ptr(q), _ptr(q_scale), _ptr(rstd), _stream(stream))
+    _check(fn, st)
+
+
+def residual_norm_workspace_bytes(rows: int, H: int) -> int:
+    """Bytes of workspace ultraep_residual_norm_backward needs for grad_weight."""
+    sz = _SZ()
+    _check("ultraep_residual_norm_workspace_bytes", lib().ultraep_residual_norm_workspace_bytes(rows, H, ctypes.byref(sz)))
+    return sz.value
+
+
+def ultraep_residual_norm_backward(ctx: Context, grad_y, h, weight, rstd, grad_h, grad_in=None, grad_x=None,
+                                   grad_weight=None, workspace=None, accumulate: bool = False, stream=None) -> None:
+    """grad_h = grad_in + the norm's gradient, grad_weight (+)= sum over the rows of grad_y * h * rstd.
+
+    grad_y bf16 [rows, H]; h, grad_in, grad_h [rows, H] of the stream's type (h: what the forward wrote, or its
+    x without a residual); grad_x bf16 [rows, H] with an fp32 stream; grad_weight fp32 [H] with a workspace of
+    residual_norm_workspace_bytes(rows, H)."""
+    fn = "ultraep_residual_norm_backward"
+    dev = _here()
+    _need(fn, h is not None and h.dim() == 2)
+    n, H = h.shape
+    w_code, h_code = _type_code(fn, weight), _type_code(fn, h)
+    own = (h.dtype,)
+    _need(fn, _is(h, dev, own, n, H) and _is(grad_y, dev, _HALVES, n, H) and _is(weight, dev, (weight.dtype,), H)
+          and _is(rstd, dev, _FLOATS, n) and _is(grad_h, dev, own, n, H) and (grad_in is None or _is(grad_in, dev, own, n, H))
+          and (grad_x is None or _is(grad_x, dev, _HALVES, n, H)) and (grad_weight is None or _is(grad_weight, dev, _FLOATS, H))
+          and (workspace is None or (workspace.get_device() == dev and workspace.is_contiguous())))
+    st = lib().ultraep_residual_norm_backward(ctx.handle, _ptr(grad_y), _ptr(h), h_code, _ptr(weight), w_code, _ptr(rstd),
+                                              _ptr(grad_in), n, H, _ptr(grad_h), _ptr(grad_x), _ptr(grad_weight),
+                                              int(accumulate), _ptr(workspace),
+                                              0 if workspace is None else workspace.numel() * workspace.element_size(),
+                                              _stream(stream))
+    _check(fn, st)
+
+
+def _glu_checks(fn: str, ctx, dev, plan, h, W: int, q, q_scale, qt, qt_scale, rows: int) -> int:
+    """Blocks of the columns form of a gated activation's results, W columns."""
+    _need(fn, (q is None) == (q_scale is None) and (qt is None) == (qt_scale is None) and not (q is None and qt is None)
+          and _is_plan(ctx, plan, dev) and 0 <= rows <= h.shape[0] and _is(h, dev, _HALVES, None, h.shape[1]))
+    if q is not None:
+        _need(fn, _is(q, dev, _BYTES, None, quant_pitch(W)) and _is(q_scale, dev, _BYTES, q.shape[0], quant_scale_pitch(W))
+              and rows <= q.shape[0])
+    if qt is None:
+        return 0
+    _need(fn, _is(qt, dev, _BYTES, None, W, QUANT_BLOCK) and _is(qt_scale, dev, _BYTES, qt.shape[0], W))
+    return qt.shape[0]
+
+
+def ultraep_glu_quant(ctx: Context, plan, h, p_begin: int, p_end: int, q=None, q_scale=None, qt=None, qt_scale=None,
+                      activation: int = GLU_SILU, rows: Optional[int] = None, stream=None) -> None:
+    """f(h[:, :F]) * h[:, F:] of the segment's rows h bf16 [., 2F], quantised.
+
+    q [., quant_pitch(F)] with q_scale [., quant_scale_pitch(F)] the rows form, qt [blocks, F, 128] with qt_scale
+    [blocks, F] the columns form.  `rows` is the segment's capacity, by default h's rows."""
+    fn = "ultraep_glu_quant"
+    dev = _here()
+    _need(fn, h is not None and h.dim() == 2 and h.shape[1] % 2 == 0)
+    F = h.shape[1] // 2
+    if rows is None:
+        rows = h.shape[0]
+    blocks = _glu_checks(fn, ctx, dev, plan, h, F, q, q_scale, qt, qt_scale, rows)
+    st = lib().ultraep_glu_quant(ctx.handle, _ptr(plan), _ptr(h), F, activation, p_begin, p_end, _ptr(q), _ptr(q_scale),
+                                 _ptr(qt), _ptr(qt_scale), rows, blocks, _stream(stream))
+    _check(fn, st)
+
+
+def ultraep_glu_quant_backward(ctx: Context, plan, h, grad, p_begin: int, p_end: int, q=None, q_scale=None, qt=None,
+                               qt_scale=None, activation: int = GLU_SILU, rows: Optional[int] = None, stream=None) -> None:
+    """Gradient rows of ultraep_glu_quant's input, quantised: grad bf16 [., F], h bf16 [., 2F] as there; q
+    [., quant_pitch(2F)], qt [blocks, 2F, 128] and their scales."""
+    fn = "ultraep_glu_quant_backward"
+    dev = _here()
+    _need(fn, h is not None and h.dim() == 2 and h.shape[1] % 2 == 0)
+    W = h.shape[1]
+    if rows is None:
+        rows = h.shape[0]
+    blocks = _glu_checks(fn, ctx, dev, plan, h, W, q, q_scale, qt, qt_scale, rows)
+    _need(fn, _is(grad, dev, _HALVES, None, W // 2) and rows <= grad.shape[0])
+    st = lib().ultraep_glu_quant_backward(ctx.handle, _ptr(plan), _ptr(h), _ptr(grad), W // 2, activation, p_begin, p_end,
+                                          _ptr(q), _ptr(q_scale), _ptr(qt), _ptr(qt_scale), rows, blocks, _stream(stream))
     _check(fn, st)
 
 

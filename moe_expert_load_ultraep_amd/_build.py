@@ -15,7 +15,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libultraep.so")
 SOURCES = ["ultraep_kernels.hip", "ultraep_combine.hip", "ultraep_weights.hip", "ultraep_abi.hip",
-           "ultraep_quant.hip", "ultraep_gemm.hip", "ultraep_grads.hip", "ultraep_experts_abi.hip"]
+           "ultraep_quant.hip", "ultraep_gemm.hip", "ultraep_grads.hip", "ultraep_experts_abi.hip",
+           "ultraep_route.hip", "ultraep_norm.hip", "ultraep_glu.hip", "ultraep_layer_abi.hip"]
 
 
 def hipcc() -> str:

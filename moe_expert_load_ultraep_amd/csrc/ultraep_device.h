@@ -162,6 +162,7 @@ __device__ __forceinline__ int32_t segment_min(int32_t x) {
 
 // 16-byte vectors as native clang vectors (the nontemporal builtins take
 // these, not HIP's struct vector types).
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
@@ -185,6 +186,36 @@ __device__ __forceinline__ float wave_sum_f32(float x) {
   x += dppf<0x141>(x);
   x += dppf<0x140>(x);
   return ((readlane_f(x, 0) + readlane_f(x, 16)) + readlane_f(x, 32)) + readlane_f(x, 48);
+}
+
+// The same in fp64: sum (one fixed order) and maximum.
+template <int CTRL>
+__device__ __forceinline__ double dpp_f64(double v) {
+  const u32x2 x = __builtin_bit_cast(u32x2, v);
+  const u32x2 y = {dpp<CTRL>(x[0]), dpp<CTRL>(x[1])};
+  return __builtin_bit_cast(double, y);
+}
+
+__device__ __forceinline__ double readlane_f64(double v, int l) {
+  const u32x2 x = __builtin_bit_cast(u32x2, v);
+  const u32x2 y = {readlane(x[0], l), readlane(x[1], l)};
+  return __builtin_bit_cast(double, y);
+}
+
+__device__ __forceinline__ double wave_sum_f64(double x) {
+  x += dpp_f64<0xB1>(x);
+  x += dpp_f64<0x4E>(x);
+  x += dpp_f64<0x141>(x);
+  x += dpp_f64<0x140>(x);
+  return ((readlane_f64(x, 0) + readlane_f64(x, 16)) + readlane_f64(x, 32)) + readlane_f64(x, 48);
+}
+
+__device__ __forceinline__ double wave_max_f64(double x) {
+  x = fmax(x, dpp_f64<0xB1>(x));
+  x = fmax(x, dpp_f64<0x4E>(x));
+  x = fmax(x, dpp_f64<0x141>(x));
+  x = fmax(x, dpp_f64<0x140>(x));
+  return fmax(fmax(readlane_f64(x, 0), readlane_f64(x, 16)), fmax(readlane_f64(x, 32), readlane_f64(x, 48)));
 }
 
 // bf16 <-> fp32: a bf16 is the top half of an fp32; fp32 -> bf16 rounds to

@@ -18,8 +18,6 @@ __host__ __device__ inline int32_t ceil_div(int32_t a, int32_t b) { return (a + 
 __host__ __device__ inline int32_t q_pitch(int32_t H) { return ceil_div(H, kQBlock) * kQBlock; }
 __host__ __device__ inline int32_t s_pitch(int32_t H) { return ceil_div(ceil_div(H, kQBlock), 4) * 4; }
 
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-
 // First row of the range's expert p, counted from the range's first row and
 // never beyond the rows that are there.
 __device__ __forceinline__ int32_t group_row(const int32_t* off, int32_t p, int64_t cap) {
@@ -158,6 +156,72 @@ __device__ __forceinline__ uint32_t to_e4m3(uint32_t pair0, uint32_t pair1, floa
 
 __device__ __forceinline__ u32x2 to_e4m3(const u32x4& x, float scale) {
   return u32x2{to_e4m3(x[0], x[1], scale), to_e4m3(x[2], x[3], scale)};
+}
+
+// The same from fp32 values: magnitudes as fp32 bits.
+constexpr uint32_t kNotFiniteF32 = 0x7F800000;
+
+__device__ __forceinline__ uint32_t magnitude(float v) { return __builtin_bit_cast(uint32_t, v) & 0x7FFFFFFFu; }
+__device__ __forceinline__ uint32_t finite_magnitude(float v) {
+  const uint32_t m = magnitude(v);
+  return m < kNotFiniteF32 ? m : 0u;
+}
+
+__device__ __forceinline__ int32_t block_exponent_f32(uint32_t amax) {
+  const int32_t e = static_cast<int32_t>(amax >> 23) - 135 + ((amax & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  return amax == 0 ? 0 : max(e, -126);
+}
+
+// Largest finite magnitude of the 16 lanes' values, as fp32 bits, in every lane.
+__device__ __forceinline__ uint32_t row16_amax(const float (&x)[8]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, magnitude(x[i]));
+  m = row16_max(m);
+  if (__builtin_expect(ballot(m >= kNotFiniteF32) != 0, 0)) {
+    m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, finite_magnitude(x[i]));
+    m = row16_max(m);
+  }
+  return m;
+}
+
+__device__ __forceinline__ uint32_t to_e4m3(float a, float b, float c, float d, float scale) {
+  i16x2 r = {0, 0};
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, a, b, scale, false);
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, c, d, scale, true);
+  return __builtin_bit_cast(uint32_t, r);
+}
+
+__device__ __forceinline__ u32x2 to_e4m3(const float (&x)[8], float scale) {
+  return u32x2{to_e4m3(x[0], x[1], x[2], x[3], scale), to_e4m3(x[4], x[5], x[6], x[7], scale)};
+}
+
+// The scale bytes of a wave's four 16-lane blocks, one word.
+__device__ __forceinline__ uint32_t four_scales(int32_t e) {
+  uint32_t s = 0;
+#pragma unroll
+  for (int b = 0; b < 4; ++b) s |= (readlane(static_cast<uint32_t>(e), 16 * b) + 127u) << (8 * b);
+  return s;
+}
+
+// 128 x 128 tiles, transposed on their way out.  A thread holds 8 x 8 values:
+// row group g = thread / 16 (rows 8g..8g+7), column group c = thread % 16.
+// Bytes wait in LDS as [column][row] with the 8-byte row groups of a column
+// exchanged by g ^ (column / 8), so that neither the stores (16 column groups
+// at once) nor the reads have bank conflicts.
+__device__ __forceinline__ void put_column_bytes(uint8_t* tile, int c, int g, const u32x2 (&b)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    *reinterpret_cast<u32x2*>(tile + (8 * c + j) * kQBlock + ((g ^ c) & 15) * 8) = b[j];
+}
+
+// 16 rows (r0 = 16 * part) of column h.
+__device__ __forceinline__ u32x4 get_column_bytes(const uint8_t* tile, int h, int part) {
+  const int c = (h >> 3) & 15;
+  const u32x4 v = *reinterpret_cast<const u32x4*>(tile + h * kQBlock + (((2 * part) ^ (c & 14)) * 8));
+  return (c & 1) ? u32x4{v[2], v[3], v[0], v[1]} : v;
 }
 
 }  // namespace

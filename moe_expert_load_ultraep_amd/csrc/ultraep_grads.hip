@@ -29,7 +29,6 @@ constexpr int kGradBlocks = ULTRAEP_GRAD_WORKSPACE_BYTES / 8;  // partial sums
 
 // Vectors at any alignment of their elements, in global memory (addresses from
 // a table would otherwise be loaded as generic ones).
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
 typedef __attribute__((address_space(1))) u32x4_any global_vec;
 typedef __attribute__((address_space(1))) uint16_t global_u16;
@@ -123,27 +122,6 @@ __device__ __forceinline__ double squares(const u32x4& v) {
     }
   }
   return s;
-}
-
-template <int CTRL>
-__device__ __forceinline__ double dpp_f64(double v) {
-  const u32x2 x = __builtin_bit_cast(u32x2, v);
-  const u32x2 y = {dpp<CTRL>(x[0]), dpp<CTRL>(x[1])};
-  return __builtin_bit_cast(double, y);
-}
-
-__device__ __forceinline__ double readlane_f64(double v, int l) {
-  const u32x2 x = __builtin_bit_cast(u32x2, v);
-  const u32x2 y = {readlane(x[0], l), readlane(x[1], l)};
-  return __builtin_bit_cast(double, y);
-}
-
-__device__ __forceinline__ double wave_sum_f64(double x) {
-  x += dpp_f64<0xB1>(x);
-  x += dpp_f64<0x4E>(x);
-  x += dpp_f64<0x141>(x);
-  x += dpp_f64<0x140>(x);
-  return ((readlane_f64(x, 0) + readlane_f64(x, 16)) + readlane_f64(x, 32)) + readlane_f64(x, 48);
 }
 
 // Sum over the workgroup, in thread 0.

@@ -96,6 +96,41 @@ hipError_t launch_grad_clip(const void* const* tensors, const int64_t* numels, i
                             const double* sumsq, double max_norm, float* norm, void* const* out,
                             hipStream_t st);
 
+// The steps around the experts (include/ultraep_layer.h).
+struct RouteArgs {
+  const void* logits;  // [tokens][E]
+  bool bf16;
+  int64_t tokens;
+  int32_t E, k;
+  bool sigmoid;
+  const float* bias;   // or null
+  int32_t groups, topk_groups, group_top;
+  bool renorm;
+  float scale;
+};
+hipError_t launch_route(const RouteArgs& a, int32_t* idx, float* w, hipStream_t st);
+hipError_t launch_route_backward(const RouteArgs& a, const int32_t* idx, const float* grad_w, void* grad_logits,
+                                 hipStream_t st);
+
+struct NormArgs {
+  int64_t rows;
+  int32_t H;
+  const void* weight;
+  bool weight_bf16;
+};
+// stream_bf16: the type of the residual stream.
+hipError_t launch_norm(const NormArgs& a, const uint16_t* x, const void* residual, bool stream_bf16, float eps,
+                       void* h, uint16_t* y, uint8_t* q, uint8_t* q_scale, float* rstd, hipStream_t st);
+size_t norm_workspace_bytes(int64_t rows, int32_t H);
+hipError_t launch_norm_backward(const NormArgs& a, const uint16_t* grad_y, const void* h, bool stream_bf16,
+                                const float* rstd, const void* grad_in, void* grad_h, uint16_t* grad_x,
+                                float* grad_weight, bool accumulate, float* partial, hipStream_t st);
+
+// grad null: the activation itself, else its gradient rows.
+hipError_t launch_glu_quant(const int32_t* off, int32_t ne, const uint16_t* h, const uint16_t* grad, int32_t F,
+                            bool gelu, uint8_t* q, uint8_t* q_scale, uint8_t* qt, uint8_t* qt_scale, int64_t cap,
+                            hipStream_t st);
+
 }  // namespace ultraep
 
 // The context behind the C ABI.
