@@ -48,7 +48,7 @@ extern "C" {
 #define ULTRAEP_GLU_SILU 0
 #define ULTRAEP_GLU_GELU 1
 
-#define ULTRAEP_MAX_NORM_WIDTH 32768
+#define ULTRAEP_MAX_NORM_WIDTH 16384
 
 /* Route tokens to their top-k experts.  For every token:
  *  1. An expert whose logit is -inf or NaN is masked: it has the score 0 and is
@@ -114,7 +114,7 @@ int ultraep_route_backward(const ultraep_ctx* ctx, const void* logits, int32_t l
  * neither each other nor what the call reads.
  * Errors: EINVAL (null x or weight with rows > 0, h without residual, half a form,
  *      no output, rows < 0, H <= 0, unknown type, eps negative or not finite);
- *      EUNSUPPORTED (H % 8 != 0, H > 32768, rows >= 2^31, x, residual, weight, h, y or
+ *      EUNSUPPORTED (H % 8 != 0, H > 16384, rows >= 2^31, x, residual, weight, h, y or
  *      q not 16-byte, q_scale or rstd not 4-byte aligned). */
 int ultraep_residual_norm(const ultraep_ctx* ctx, const uint16_t* x, const void* residual,
                           int32_t residual_type, const void* weight, int32_t weight_type, float eps,
@@ -141,7 +141,7 @@ int ultraep_residual_norm_workspace_bytes(int64_t rows, int32_t H, size_t* out);
  *      looked at without grad_weight.
  * Errors: EINVAL (null pointers with rows > 0, a grad_weight without workspace,
  *      grad_x with a bf16 stream, rows < 0, H <= 0, unknown type, accumulate not 0 or
- *      1); EUNSUPPORTED (H % 8 != 0, H > 32768, rows >= 2^31, a buffer not 16-byte,
+ *      1); EUNSUPPORTED (H % 8 != 0, H > 16384, rows >= 2^31, a buffer not 16-byte,
  *      rstd not 4-byte aligned); EWORKSPACE. */
 int ultraep_residual_norm_backward(const ultraep_ctx* ctx, const uint16_t* grad_y, const void* h,
                                    int32_t h_type, const void* weight, int32_t weight_type,

@@ -108,7 +108,7 @@ _LAYER_SIGNATURES = {
 }
 ROUTE_SOFTMAX, ROUTE_SIGMOID = 0, 1
 GLU_SILU, GLU_GELU = 0, 1
-MAX_ROUTE_GROUPS, MAX_NORM_WIDTH = 64, 32768
+MAX_ROUTE_GROUPS, MAX_NORM_WIDTH = 64, 16384
 QUANT_BLOCK = 128
 MAX_GRAD_TENSORS = 4096
 GRAD_WORKSPACE_BYTES = 16384

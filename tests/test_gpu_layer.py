@@ -242,7 +242,7 @@ def check_cols_form(qt, scale, want, rel, off, blocks):
 
 # ---------------------------------------------------------------- norm
 
-WIDTHS = [8, 64, 120, 128, 520, 1000, 2048, 2056, 4096, 5120, 7168, 8192, 8200, 16384, 16392, 32768]
+WIDTHS = [8, 64, 120, 128, 512, 520, 1000, 1024, 1032, 2048, 2056, 4096, 5120, 7168, 8192, 8200, 16384]
 
 
 def stream_of(x, dtype):

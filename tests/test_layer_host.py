@@ -74,7 +74,7 @@ def test_residual_norm_refusals(ctx):
     for bad in (dict(c=None), dict(x=None), dict(w=None), dict(r=None), dict(q=None), dict(qs=None), dict(rt=2), dict(wt=-1), dict(n=-1),
                 dict(H=0), dict(e=-1e-6), dict(e=NAN), dict(e=INF), dict(h=None, y=None, q=None, qs=None, v=None)):
         assert call(**bad) == -1, bad
-    for bad in (dict(H=12), dict(H=32776), dict(n=1 << 31), dict(x=F + 8), dict(r=F + 8), dict(w=F + 8), dict(h=F + 8), dict(y=F + 8),
+    for bad in (dict(H=12), dict(H=16392), dict(n=1 << 31), dict(x=F + 8), dict(r=F + 8), dict(w=F + 8), dict(h=F + 8), dict(y=F + 8),
                 dict(q=F + 8), dict(qs=F + 2), dict(v=F + 2)):
         assert call(**bad) == -2, bad
     assert call(n=0, x=None, r=None, w=None, h=None, y=None, q=None, qs=None, v=None) == 0
@@ -91,12 +91,12 @@ def test_residual_norm_backward_refusals(ctx):
     for bad in (dict(c=None), dict(g=None), dict(h=None), dict(w=None), dict(v=None), dict(gh=None), dict(ws=None), dict(ht=1), dict(ht=2),
                 dict(wt=2), dict(n=-1), dict(H=-8), dict(acc=2)):
         assert call(**bad) == -1, bad
-    for bad in (dict(H=12), dict(H=32776), dict(n=1 << 31), dict(g=F + 8), dict(h=F + 8), dict(w=F + 8), dict(v=F + 2), dict(gi=F + 8),
+    for bad in (dict(H=12), dict(H=16392), dict(n=1 << 31), dict(g=F + 8), dict(h=F + 8), dict(w=F + 8), dict(v=F + 2), dict(gi=F + 8),
                 dict(gh=F + 8), dict(gx=F + 8), dict(gw=F + 8), dict(ws=F + 8)):
         assert call(**bad) == -2, bad
     assert call(b=need - 1) == -4
     assert call(n=0, g=None, h=None, w=None, v=None, gi=None, gh=None, gx=None, gw=None, ws=None) == 0
-    for n, H, status in ((-1, 64, -1), (1, 0, -1), (1, 12, -2), (1, 32776, -2), (1 << 31, 64, -2)):
+    for n, H, status in ((-1, 64, -1), (1, 0, -1), (1, 12, -2), (1, 16392, -2), (1 << 31, 64, -2)):
         assert U.lib().ultraep_residual_norm_workspace_bytes(n, H, ctypes.byref(size)) == status
     assert U.lib().ultraep_residual_norm_workspace_bytes(1, 64, None) == -1
     assert U.residual_norm_workspace_bytes(10, 64) == need
