@@ -9,9 +9,6 @@
 #include "ultraep_device.h"
 #include "ultraep_internal.h"
 
-#ifndef ROUTE_V1
-#define ROUTE_V1 1024
-#endif
 namespace ultraep {
 namespace {
 
@@ -26,23 +23,31 @@ __device__ __forceinline__ float load_logit(const RouteArgs& a, int64_t at) {
   return clean_logit(a.bf16 ? bf16_lo(static_cast<const uint16_t*>(a.logits)[at]) : static_cast<const float*>(a.logits)[at]);
 }
 
+// The lanes of a wave see each other's LDS.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+__device__ __forceinline__ float f32_of(uint32_t bits) { return __builtin_bit_cast(float, bits); }
+
 __device__ __forceinline__ bool masked(float l) { return l == -__builtin_huge_valf(); }
 
-// Softmax: largest logit and 1 / sum over the wave's logits (V a lane).
+// Softmax: largest logit and 1 / sum.
 struct Soft {
   double m, inv;
 };
 
-template <int V>
-__device__ __forceinline__ Soft soft_of(const float (&l)[V]) {
-  float m = l[0];
-#pragma unroll
-  for (int v = 1; v < V; ++v) m = fmaxf(m, l[v]);
+// Of one token's logits, by one wave.
+__device__ __forceinline__ Soft soft_of(const RouteArgs& a, int64_t t) {
+  float m = -__builtin_huge_valf();
+  for (int32_t e = lane_id(); e < a.E; e += 64) m = fmaxf(m, load_logit(a, t * a.E + e));
   Soft s{wave_max_f64(static_cast<double>(m)), 0.0};
   double sum = 0.0;
-#pragma unroll
-  for (int v = 0; v < V; ++v)
-    if (!masked(l[v])) sum += exp(static_cast<double>(l[v]) - s.m);
+  for (int32_t e = lane_id(); e < a.E; e += 64) {
+    const float l = load_logit(a, t * a.E + e);
+    if (!masked(l)) sum += exp(static_cast<double>(l) - s.m);
+  }
   s.inv = 1.0 / wave_sum_f64(sum);
   return s;
 }
@@ -71,50 +76,42 @@ __device__ __forceinline__ double weight_of(const RouteArgs& a, bool some, float
   return some ? a.scale * t / sum : 0.0;
 }
 
-// One token by one wave, expert e = lane + 64 v in lane e % 64, all in fp64.  keys: room
-// for E fp64 of the wave's own where there are groups.
-template <int V>
+// One token by one wave, all in fp64.  keys: E fp64 of the wave's own, expert e's written
+// and read by lane e % 64 (but for the groups').
 __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, double* keys, int32_t* __restrict__ topk_idx,
                                             float* __restrict__ topk_w) {
   const int lane = lane_id();
-  const int32_t per = a.E / a.groups;
-  float l[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int e = lane + 64 * v;
-    l[v] = e < a.E ? load_logit(a, t * a.E + e) : -__builtin_huge_valf();
-  }
   Soft soft{0.0, 0.0};
-  if (!a.sigmoid) soft = soft_of(l);
-  double key[V];
+  if (!a.sigmoid) soft = soft_of(a, t);
+  // logits (and biases) of four experts at once, as this is mostly waiting
+  const bool sums = a.groups > 1 && a.group_top == 2;  // of scores, also where the keys are the logits
+  for (int32_t e0 = lane; e0 < a.E; e0 += 256) {
+    float l[4], b[4];
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int e = lane + 64 * v;
-    key[v] = kNone;
-    if (masked(l[v])) continue;
-    if (a.bias == nullptr) {
-      key[v] = static_cast<double>(l[v]);
-    } else {
-      const double x = score_of(a.sigmoid, l[v], soft) + static_cast<double>(a.bias[e]);
-      key[v] = x == x ? x : kNone;
+    for (int i = 0; i < 4; ++i) {
+      const int32_t e = min(e0 + 64 * i, a.E - 1);
+      l[i] = load_logit(a, t * a.E + e);
+      b[i] = a.bias != nullptr ? a.bias[e] : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      double key = static_cast<double>(l[i]);
+      if (!masked(l[i]) && (sums || a.bias != nullptr)) key = score_of(a.sigmoid, l[i], soft) + static_cast<double>(b[i]);
+      if (e0 + 64 * i < a.E) keys[e0 + 64 * i] = key == key ? key : kNone;
     }
   }
   if (a.groups > 1) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int e = lane + 64 * v;
-      if (e < a.E)
-        keys[e] = a.bias == nullptr && a.group_top == 2 && key[v] != kNone ? score_of(a.sigmoid, l[v], soft) : key[v];
-    }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+    const int32_t per = a.E / a.groups;
+    wave_sync();
     double first = kNone, second = kNone;
-    if (lane < a.groups)
+    if (lane < a.groups) {
+#pragma unroll 8
       for (int i = 0; i < per; ++i) {
         const double x = keys[lane * per + i];
         second = fmax(second, fmin(first, x));
         first = fmax(first, x);
       }
+    }
     const double worth = a.group_top == 2 && second != kNone ? first + second : first;
     int rank = 0;
     for (int g = 0; g < a.groups; ++g) {
@@ -122,32 +119,29 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, doubl
       rank += x > worth || (x == worth && g < lane);
     }
     const uint64_t taken = ballot(lane < a.groups && worth != kNone && rank < a.topk_groups);
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int e = lane + 64 * v;
-      if (e < a.E && !((taken >> (e / per)) & 1)) key[v] = kNone;
+    wave_sync();
+    for (int32_t e = lane; e < a.E; e += 64) {
+      if (sums && a.bias == nullptr && keys[e] != kNone) keys[e] = static_cast<double>(load_logit(a, t * a.E + e));
+      if (!((taken >> (e / per)) & 1)) keys[e] = kNone;
     }
   }
   int32_t mine = -1;  // lane j: the j-th expert
   for (int j = 0; j < a.k; ++j) {
-    double best = key[0];
-    int at = 0;
-#pragma unroll
-    for (int v = 1; v < V; ++v)
-      if (key[v] > best) {
-        best = key[v];
-        at = v;
+    double best = kNone;
+    int32_t at = lane;
+#pragma unroll 4
+    for (int32_t e = lane; e < a.E; e += 64) {
+      const double x = keys[e];
+      if (x > best) {
+        best = x;
+        at = e;
       }
+    }
     const double top = wave_max_f64(best);
     if (top == kNone) break;  // the same in every lane
-    const uint32_t e = lane + 64 * at;
-    const uint32_t win = ~wave_max(best == top ? ~e : 0u);  // the lowest id
-    if (lane == j) mine = static_cast<int32_t>(win);
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (lane + 64 * v == static_cast<int>(win)) key[v] = kNone;
+    const int32_t win = static_cast<int32_t>(~wave_max(best == top ? ~static_cast<uint32_t>(at) : 0u));  // the lowest id
+    if (lane == j) mine = win;
+    if (lane == win % 64) keys[win] = kNone;
   }
   const bool some = mine >= 0;
   const float lj = some ? load_logit(a, t * a.E + mine) : 0.f;
@@ -158,14 +152,13 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, doubl
   }
 }
 
-template <int V>
 __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a, int32_t* __restrict__ topk_idx,
                                                               float* __restrict__ topk_w) {
   extern __shared__ double s_keys[];
   const int wv = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
   const int64_t nwaves = static_cast<int64_t>(gridDim.x) * kRouteWaves;
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteWaves + wv; t < a.tokens; t += nwaves)
-    route_token<V>(a, t, s_keys + wv * a.E, topk_idx, topk_w);
+    route_token(a, t, s_keys + wv * a.E, topk_idx, topk_w);
 }
 
 // ---------------------------------------------------------------------------
@@ -245,7 +238,7 @@ __device__ __forceinline__ float fast_sigmoid(float l) {
 
 // Words of a token's row of keys in LDS: 16 more than a multiple of 64, so that the rows
 // of neighbouring tokens start in different banks.
-__host__ __device__ inline int32_t key_pitch(int32_t E) { return E + ((16 - E) & 63); }
+__host__ __device__ inline int32_t key_pitch(int32_t E) { return E + ((16 - E) & 63); }  // a multiple of 16
 
 struct KeyUnits {
   float c;        // units of a score
@@ -290,47 +283,77 @@ __device__ __forceinline__ KeyUnits bias_units(const RouteArgs& a, float* table)
   return u;
 }
 
+// Words of LDS a wave has for itself: keys and worths of its tokens' groups, or E fp64.
+template <int LPT>
+__host__ __device__ inline int32_t wave_words(const RouteArgs& a) {
+  return a.groups > 1 ? 64 / LPT * (key_pitch(a.E) + kFastGroups) : 2 * a.E;
+}
+
 template <int LPT, int NI, int KL>
-__global__ __launch_bounds__(kRouteThreads) void route_fast_kernel(RouteArgs a, int32_t* __restrict__ topk_idx,
+__global__ __launch_bounds__(kRouteThreads, NI > 10 ? 3 : 4) void route_fast_kernel(RouteArgs a, int32_t* __restrict__ topk_idx,
                                                                    float* __restrict__ topk_w) {
   extern __shared__ __align__(16) char s_dyn[];
   using P = Packed<LPT>;
-  constexpr int kTokens = 64 / LPT, kAll = LPT * NI * 4, V = (kAll + 63) / 64, MM = (KL - 1 + LPT - 1) / LPT;
+  constexpr int kTokens = 64 / LPT, kAll = LPT * NI * 4, MM = (KL - 1 + LPT - 1) / LPT;
   constexpr float kHigh = P::kTop - 64.f, kPerLogit = kHigh / kLogitRange;
-  const int lane = lane_id(), q = lane % LPT, tl = lane / LPT;
   const int wv = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
-  const int32_t E = a.E, per = E / a.groups, pitch = key_pitch(E);
+  const int32_t per = a.E / a.groups, pitch = key_pitch(a.E);
   float* bias = reinterpret_cast<float*>(s_dyn);  // [kAll]
-  uint32_t* keys = reinterpret_cast<uint32_t*>(s_dyn) + kAll + wv * kTokens * (pitch + kFastGroups);
+  uint32_t* keys = reinterpret_cast<uint32_t*>(s_dyn) + kAll + wv * wave_words<LPT>(a);
   float* worths = reinterpret_cast<float*>(keys + kTokens * pitch);
   const bool with_bias = a.bias != nullptr;
+  const bool in_fours = a.E % 4 == 0 && reinterpret_cast<uintptr_t>(a.logits) % 8 == 0;  // bf16
   KeyUnits units{0.f, false};
   if (with_bias) units = bias_units<LPT, NI>(a, bias);
   // what two keys have to be apart for their order to be certain, in units
-  const uint32_t margin = with_bias ? (a.sigmoid ? 16u : 64u) : a.bf16 ? 0u : 8u;
-  const int64_t nwaves = static_cast<int64_t>(gridDim.x) * kRouteWaves;
-  for (int64_t batch = static_cast<int64_t>(blockIdx.x) * kRouteWaves + wv; batch * kTokens < a.tokens; batch += nwaves) {
-    const int64_t t = batch * kTokens + tl, tok = min(t, a.tokens - 1);
-    // logits
-    float l[4 * NI];
-    const auto logit_chunk = [&](int i, float (&x)[4]) {
-      const int e = (i * LPT + q) * 4, at = e < E ? e : 0;
-      if (a.bf16) {
-        const u32x2 v = *reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(a.logits) + tok * E + at);
-        x[0] = bf16_lo(v[0]), x[1] = bf16_hi(v[0]), x[2] = bf16_lo(v[1]), x[3] = bf16_hi(v[1]);
-      } else {
-        const f32x4 v = *reinterpret_cast<const f32x4*>(static_cast<const float*>(a.logits) + tok * E + at);
-        x[0] = v[0], x[1] = v[1], x[2] = v[2], x[3] = v[3];
+  const uint32_t margin = with_bias ? (a.sigmoid ? (LPT == 4 ? 13u : 9u) : (LPT == 4 ? 64u : 40u)) : a.bf16 ? 0u : 8u;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kRouteWaves;
+  float l[4 * NI];
+  // A batch's logits through one resource: an address a lane, chunks at constant
+  // distances; what is behind a row is the next one's, or zeros behind the last.
+  const auto load = [&](int64_t batch, int lane, int32_t E) {
+    const int q = lane % LPT, tl = lane / LPT, size = a.bf16 ? 2 : 4;
+    const int64_t left = min(a.tokens - batch * kTokens, static_cast<int64_t>(kTokens));
+    const __amdgpu_buffer_rsrc_t rows = row_rsrc(static_cast<const char*>(a.logits) + batch * kTokens * E * size,
+                                                 left > 0 ? static_cast<uint32_t>(left * E * size) : 0u);
+    const int from = (tl * E + 4 * q) * size;
+    if (!a.bf16) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(rows, from + i * LPT * 16, 0, 0);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) l[4 * i + c] = f32_of(v[c]);
       }
-      if (e >= E) x[0] = x[1] = x[2] = x[3] = -__builtin_huge_valf();
-    };
+    } else if (in_fours) {
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      float x[4];
-      logit_chunk(i, x);
+      for (int i = 0; i < NI; ++i) {
+        const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(rows, from + i * LPT * 8, 0, 0);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) l[4 * i + c] = x[c];
+        for (int c = 0; c < 4; ++c) l[4 * i + c] = c & 1 ? bf16_hi(v[c / 2]) : bf16_lo(v[c / 2]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4 * NI; ++i)
+        l[i] = bf16_lo(__builtin_amdgcn_raw_buffer_load_b16(rows, from + (i / 4 * LPT * 4 + i % 4) * 2, 0, 0));
     }
+  };
+  int64_t batch = static_cast<int64_t>(blockIdx.x) * kRouteWaves + wv;
+  load(batch, lane_id(), a.E);
+  for (; batch * kTokens < a.tokens; batch += step) {
+    // Made anew in every round: what hangs on them is cheap, and kept in registers (a
+    // few for every expert of the lane) would push the logits out.
+    int lane = lane_id();
+    int32_t E = a.E;
+    asm volatile("" : "+v"(lane), "+s"(E));
+    const int q = lane % LPT, tl = lane / LPT;
+    const int64_t t = batch * kTokens + tl;
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+      if ((i + 1) * LPT * 4 > E) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if ((i * LPT + q) * 4 + c >= E) l[4 * i + c] = -__builtin_huge_valf();
+      }
     float top = -__builtin_huge_valf(), inv = 0.f;
     bool again = units.exact;
     if (!(with_bias && a.sigmoid)) {
@@ -347,72 +370,81 @@ __global__ __launch_bounds__(kRouteThreads) void route_fast_kernel(RouteArgs a, 
       again |= total != total && top > -__builtin_huge_valf();  // a NaN among them
       inv = 1.f / total;
     }
-    // Keys, four at a time into LDS (where there are groups) or into the lane's list.
+    // Keys, of values that are numbers: into LDS where there are groups, else into the
+    // lane's list.  Not everything at once, which would take more registers than there are.
     uint32_t list[KL];
 #pragma unroll
     for (int j = 0; j < KL; ++j) list[j] = 0;
-    int ids = static_cast<int>(P::kIds) - 4 * q;
-    asm volatile("" : "+v"(ids));  // made anew for every key: kept in registers they would be 4 * NI
-    const auto pack = [&](int i, int c, uint32_t value) {
-      return (value << P::kIdBits) | static_cast<uint32_t>(ids - (i * LPT * 4 + c));
-    };
-    // the value of an fp32 logit without a bias (NaN and masked ones: 0)
-    const auto logit_value = [&](float x) {
-      return static_cast<uint32_t>(x == x ? fmaxf(__builtin_fmaf(x - top, kPerLogit, kHigh), 0.f) : 0.f);
-    };
-    const auto put = [&](int i, const uint32_t (&key)[4]) {
-      const int e = (i * LPT + q) * 4;
+    const int ids = static_cast<int>(P::kIds) - 4 * q;
+    const auto make_keys = [&](auto&& values) {  // of a chunk
+      const auto chunk = [&](int i, uint32_t (&key)[4]) {
+        float x[4];
+        values(i, x);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) key[c] = (static_cast<uint32_t>(x[c]) << P::kIdBits) | static_cast<uint32_t>(ids - (i * LPT * 4 + c));
+        if (i % 2 == 1) __builtin_amdgcn_sched_barrier(0);
+      };
       if (a.groups > 1) {
-        if (e < E) *reinterpret_cast<u32x4*>(keys + tl * pitch + e) = u32x4{key[0], key[1], key[2], key[3]};
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          uint32_t key[4];
+          chunk(i, key);
+          if ((i * LPT + q) * 4 < E)
+            *reinterpret_cast<u32x4*>(keys + tl * pitch + (i * LPT + q) * 4) = u32x4{key[0], key[1], key[2], key[3]};
+        }
       } else {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) insert<0>(list, key[c]);
+        for (int i = 0; i < NI; ++i) {
+          uint32_t key[4];
+          chunk(i, key);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) insert<0>(list, key[c]);
+        }
       }
     };
+    const auto logit_value = [&](float x) { return __builtin_fmaf(x - top, kPerLogit, kHigh); };  // NaN or below 0: 0
     if (with_bias) {
+      float low = l[0];
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const f32x4 b = *reinterpret_cast<const f32x4*>(bias + (i * LPT + q) * 4);
-        uint32_t key[4];
+      for (int i = 1; i < 4 * NI; ++i) low = fminf(low, l[i]);
+      if (ballot(low == -__builtin_huge_valf()) != 0) {  // a masked expert's score is 0, which would be a key
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float x = l[4 * i + c], s = a.sigmoid ? fast_sigmoid(x) : __builtin_amdgcn_exp2f((x - top) * kLog2e) * inv;
-          key[c] = pack(i, c, static_cast<uint32_t>(__builtin_fmaf(s, units.c, b[c])));  // NaN: 0
-        }
-        // a masked logit's score is 0, which is a key; NaN is none already
-        if (ballot(fminf(fminf(l[4 * i], l[4 * i + 1]), fminf(l[4 * i + 2], l[4 * i + 3])) == -__builtin_huge_valf()) != 0) {
+        for (int i = 0; i < 4 * NI; ++i) l[i] = masked(l[i]) ? __builtin_nanf("") : l[i];
+      }
+      const float* b = bias + 4 * q;
+      if (a.sigmoid)
+        make_keys([&](int i, float (&x)[4]) {
+          const f32x4 add = *reinterpret_cast<const f32x4*>(b + i * LPT * 4);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) x[c] = __builtin_fmaf(fast_sigmoid(l[4 * i + c]), units.c, add[c]);
+        });
+      else
+        make_keys([&](int i, float (&x)[4]) {
+          const f32x4 add = *reinterpret_cast<const f32x4*>(b + i * LPT * 4);
 #pragma unroll
           for (int c = 0; c < 4; ++c)
-            if (masked(l[4 * i + c])) key[c] = 0;
-        }
-        put(i, key);
-      }
+            x[c] = __builtin_fmaf(__builtin_amdgcn_exp2f((l[4 * i + c] - top) * kLog2e) * inv, units.c, add[c]);
+        });
     } else if (a.bf16) {
       // the 16 bits themselves, in ascending order: nothing is lost
-#pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        uint32_t key[4];
+      make_keys([&](int i, float (&x)[4]) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const float x = l[4 * i + c];
-          uint32_t u = __builtin_bit_cast(uint32_t, x == 0.f ? 0.f : x);
+          const float y = l[4 * i + c];
+          uint32_t u = __builtin_bit_cast(uint32_t, y == 0.f ? 0.f : y);
           u ^= static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u;
-          key[c] = x > -__builtin_huge_valf() ? pack(i, c, (u >> 16) + 1) : 0u;
+          x[c] = y > -__builtin_huge_valf() ? static_cast<float>((u >> 16) + 1) : 0.f;
         }
-        put(i, key);
-      }
+      });
     } else {
+      make_keys([&](int i, float (&x)[4]) {
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        uint32_t key[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) key[c] = pack(i, c, logit_value(l[4 * i + c]));
-        put(i, key);
-      }
+        for (int c = 0; c < 4; ++c) x[c] = logit_value(l[4 * i + c]);
+      });
     }
+    load(batch + step, lane, E);  // the next round's, on their way while this one's are chosen
     if (a.groups > 1) {
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
+      wave_sync();
       constexpr int kOwn = kFastGroups / LPT;
       float worth[kOwn];
       const uint32_t* row = keys + tl * pitch;
@@ -465,15 +497,15 @@ __global__ __launch_bounds__(kRouteThreads) void route_fast_kernel(RouteArgs a, 
           if (g < a.groups) worths[tl * kFastGroups + g] = worth[gi];
         }
       }
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
+      wave_sync();
       int rank[kOwn];
 #pragma unroll
       for (int gi = 0; gi < kOwn; ++gi) rank[gi] = 0;
       for (int g = 0; g < a.groups; ++g) {
         const float x = worths[tl * kFastGroups + g];
 #pragma unroll
-        for (int gi = 0; gi < kOwn; ++gi) rank[gi] += x > worth[gi] || (x == worth[gi] && g < gi * LPT + q);
+        for (int gi = 0; gi < kOwn; ++gi)
+          if (gi * LPT < a.groups) rank[gi] += x > worth[gi] || (x == worth[gi] && g < gi * LPT + q);
       }
       uint32_t taken = 0;
       float in = __builtin_huge_valf(), out = -__builtin_huge_valf();
@@ -517,24 +549,51 @@ __global__ __launch_bounds__(kRouteThreads) void route_fast_kernel(RouteArgs a, 
       for (int j = 0; j < KL; ++j) other[j] = dpp<decltype(ctrl)::value>(list[j]);
       insert_all<0>(list, other);
     });
-    // is every order that counts certain?
-    uint32_t last = 0;
+    // Is every order that counts certain?  One that is not, of two chosen, is settled by
+    // their keys in fp64; anything else is for route_token.
+    uint32_t last = 0, close = 0, upper = 0, lower = 0;
+    int place = 0;
 #pragma unroll
     for (int j = 0; j < KL - 1; ++j) {
       if (j >= a.k) continue;
       const uint32_t x = list[j] >> P::kIdBits, y = list[j + 1] >> P::kIdBits;
-      again |= y != 0 && x - y < margin;
       last = x;
+      if (y != 0 && x - y < margin) {
+        if (j + 1 >= a.k) again = true;
+        close += 1;
+        place = j;
+        upper = list[j];
+        lower = list[j + 1];
+      }
     }
-    if (!with_bias && !a.bf16 && ballot(last < margin) != 0) {
-      // fewer experts than k, or logits below the keys' range: are there such?
-      int unseen = 0;
+    again |= close > 1;
+    const bool settle = close == 1 && !again && t < a.tokens;
+    if (ballot(settle) != 0) {
+      if (with_bias && !a.sigmoid) {
+        again |= settle;  // their scores hang on all of the row
+      } else {
+        const int32_t e0 = static_cast<int32_t>(P::kIds - (upper & P::kIds)), e1 = static_cast<int32_t>(P::kIds - (lower & P::kIds));
+        double k0 = 0.0, k1 = 0.0;
+        if (settle) {
+          const float l0 = load_logit(a, t * E + e0), l1 = load_logit(a, t * E + e1);
+          k0 = with_bias ? score_of(true, l0, Soft{}) + static_cast<double>(a.bias[e0]) : static_cast<double>(l0);
+          k1 = with_bias ? score_of(true, l1, Soft{}) + static_cast<double>(a.bias[e1]) : static_cast<double>(l1);
+        }
+        const bool swap = settle && (k1 > k0 || (k1 == k0 && e1 < e0));
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        float x[4];
-        logit_chunk(i, x);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) unseen |= x[c] > -__builtin_huge_valf() && logit_value(x[c]) < margin;
+        for (int j = 0; j < KL - 2; ++j) {
+          if (swap && j == place) {
+            list[j] = lower;
+            list[j + 1] = upper;
+          }
+        }
+      }
+    }
+    if (!with_bias && ballot(last < margin) != 0) {  // fewer than k: are there any below the keys' range?
+      uint32_t unseen = 0;
+      for (int e = q; e < E && t < a.tokens; e += LPT) {
+        const float x = load_logit(a, t * E + e);
+        unseen |= !masked(x) && logit_value(x) < static_cast<float>(margin);
       }
       again |= last < margin && token_or<LPT>(unseen) != 0;
     }
@@ -548,9 +607,9 @@ __global__ __launch_bounds__(kRouteThreads) void route_fast_kernel(RouteArgs a, 
 #pragma unroll
       for (int c = 0; c < LPT; ++c)
         if (mm * LPT + c < KL - 1) k_j = q == c ? list[mm * LPT + c < KL ? mm * LPT + c : 0] : k_j;
-      const bool some = (k_j >> P::kIdBits) != 0 && mm * LPT + q < a.k;
+      const bool some = (k_j >> P::kIdBits) != 0 && mm * LPT + q < a.k && t < a.tokens;
       e_j[mm] = some ? static_cast<int32_t>(P::kIds - (k_j & P::kIds)) : -1;
-      l_j[mm] = some ? load_logit(a, tok * E + e_j[mm]) : 0.f;
+      l_j[mm] = some ? load_logit(a, t * E + e_j[mm]) : 0.f;
       if (some) m = fmaxf(m, l_j[mm]);
     }
     m = token_max<LPT>(m);
@@ -575,12 +634,10 @@ __global__ __launch_bounds__(kRouteThreads) void route_fast_kernel(RouteArgs a, 
         topk_w[t * a.k + j] = e_j[mm] < 0 ? 0.f : w[mm] * factor;
       }
     }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+    wave_sync();
     for (uint64_t redo = ballot(again && q == 0 && t < a.tokens); redo != 0; redo &= redo - 1)
-      route_token<V>(a, batch * kTokens + __builtin_ctzll(redo) / LPT, reinterpret_cast<double*>(keys), topk_idx, topk_w);
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+      route_token(a, batch * kTokens + __builtin_ctzll(redo) / LPT, reinterpret_cast<double*>(keys), topk_idx, topk_w);
+    wave_sync();
   }
 }
 
@@ -603,7 +660,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(RouteArgs
         const int e = lane + 64 * v;
         l[v] = e < a.E ? load_logit(a, t * a.E + e) : -__builtin_huge_valf();
       }
-      soft = soft_of(l);
+      soft = soft_of(a, t);
     }
     int32_t e_j = lane < a.k ? topk_idx[t * a.k + lane] : -1;
     if (e_j < 0 || e_j >= a.E) e_j = -1;
@@ -652,8 +709,10 @@ namespace {
 template <int LPT, int NI, int KL>
 void launch_fast(const RouteArgs& a, int32_t* idx, float* w, hipStream_t st) {
   constexpr int kTokens = 64 / LPT;
-  const size_t lds = 4 * (LPT * NI * 4 + (a.groups > 1 ? kRouteWaves * kTokens * (key_pitch(a.E) + kFastGroups) : 0));
-  const int64_t want = (a.tokens + kTokens * kRouteWaves - 1) / (kTokens * kRouteWaves), most = ROUTE_V1;
+  const size_t lds = 4 * (LPT * NI * 4 + kRouteWaves * wave_words<LPT>(a));
+  // as many workgroups as fit the CUs at once, by registers (three or four) and by LDS
+  const int64_t fit = NI > 10 ? 3 : 4, by_lds = (160 << 10) / static_cast<int64_t>(lds);
+  const int64_t want = (a.tokens + kTokens * kRouteWaves - 1) / (kTokens * kRouteWaves), most = 256 * (fit < by_lds ? fit : by_lds);
   hipLaunchKernelGGL((route_fast_kernel<LPT, NI, KL>), dim3(static_cast<uint32_t>(want < most ? want : most)), dim3(kRouteThreads),
                      lds, st, a, idx, w);
 }
@@ -664,10 +723,7 @@ void launch_fast_of(const RouteArgs& a, int32_t* idx, float* w, hipStream_t st) 
 }
 
 // Whether the kernel for many tokens a wave takes the call.
-bool fast_route(const RouteArgs& a) {
-  const size_t unit = a.bf16 ? 8 : 16;
-  return a.k <= 12 && a.E <= 512 && a.E % 4 == 0 && a.groups <= kFastGroups && reinterpret_cast<uintptr_t>(a.logits) % unit == 0;
-}
+bool fast_route(const RouteArgs& a) { return a.k <= 12 && a.E <= 512 && a.groups <= kFastGroups; }
 
 }  // namespace
 
@@ -687,14 +743,7 @@ hipError_t launch_route(const RouteArgs& args, int32_t* idx, float* w, hipStream
     go(a, idx, w, st);
     return hipGetLastError();
   }
-  const size_t lds = a.groups > 1 ? kRouteWaves * a.E * sizeof(double) : 0;
-  const dim3 grid(route_grid(a.tokens)), block(kRouteThreads);
-  if (a.E <= 64)
-    hipLaunchKernelGGL(route_kernel<1>, grid, block, lds, st, a, idx, w);
-  else if (a.E <= 256)
-    hipLaunchKernelGGL(route_kernel<4>, grid, block, lds, st, a, idx, w);
-  else
-    hipLaunchKernelGGL(route_kernel<16>, grid, block, lds, st, a, idx, w);
+  hipLaunchKernelGGL(route_kernel, dim3(route_grid(a.tokens)), dim3(kRouteThreads), kRouteWaves * a.E * sizeof(double), st, a, idx, w);
   return hipGetLastError();
 }
 
