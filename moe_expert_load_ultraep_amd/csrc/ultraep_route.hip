@@ -641,59 +641,192 @@ __global__ __launch_bounds__(kRouteThreads, NI > 10 ? 3 : 4) void route_fast_ker
   }
 }
 
-// One wave a token: lane j < k has the j-th chosen expert's gradient, every lane the
-// elements e = lane + 64 v of the row.
-template <int V>
+// ---------------------------------------------------------------------------
+// Gradients.  LPT lanes have a token, lane q its chosen experts j = q, q + LPT, ...; the
+// tokens' rows are put together in LDS and go out as one stream of whole lines.
+template <int LPT>
+__host__ __device__ inline int32_t grad_words(int32_t E) { return 64 / LPT * key_pitch(E); }
+
+// Where the same id stands more than once in a row, the first takes all their gradients,
+// added up in the order of the row, and the others none.
+template <int LPT, int MM>
+__device__ __forceinline__ void merge_same(int32_t (&e)[MM], float (&d)[MM]) {
+  const int lane = lane_id(), q = lane % LPT, first = lane - q;
+  float sum[MM];
+  bool later[MM];
+#pragma unroll
+  for (int mm = 0; mm < MM; ++mm) sum[mm] = 0.f, later[mm] = false;
+#pragma unroll
+  for (int nn = 0; nn < MM; ++nn)
+    for (int c = 0; c < LPT; ++c) {
+      const int32_t other = __shfl(e[nn], first + c);
+      const float x = __shfl(d[nn], first + c);
+#pragma unroll
+      for (int mm = 0; mm < MM; ++mm) {
+        if (other != e[mm]) continue;
+        sum[mm] += x;
+        later[mm] |= nn * LPT + c < mm * LPT + q;
+      }
+    }
+#pragma unroll
+  for (int mm = 0; mm < MM; ++mm) {
+    if (e[mm] >= 0) d[mm] = sum[mm];
+    if (later[mm]) e[mm] = -1;
+  }
+}
+
+template <int LPT, int MM>
 __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(RouteArgs a, const int32_t* __restrict__ topk_idx,
                                                                        const float* __restrict__ grad_w,
                                                                        void* __restrict__ grad_logits) {
-  const int lane = lane_id();
+  extern __shared__ __align__(16) float s_rows[];
+  constexpr int kTokens = 64 / LPT;
+  const int lane = lane_id(), q = lane % LPT, tl = lane / LPT;
   const int wv = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
-  const int64_t nwaves = static_cast<int64_t>(gridDim.x) * kRouteWaves;
+  const int32_t E = a.E, pitch = key_pitch(E), words = grad_words<LPT>(E);
+  float* rows = s_rows + wv * words;
+  float* row = rows + tl * pitch;
   const bool every = !a.sigmoid && !a.renorm;
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteWaves + wv; t < a.tokens; t += nwaves) {
-    float l[V];
-    Soft soft{0.0, 0.0};
+  const bool in_fours = E % 4 == 0 && reinterpret_cast<uintptr_t>(grad_logits) % (a.bf16 ? 8 : 16) == 0;
+  const bool logits_in_fours = E % 4 == 0 && reinterpret_cast<uintptr_t>(a.logits) % (a.bf16 ? 8 : 16) == 0;
+  const float per_row = 1.f / static_cast<float>(E);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kRouteWaves;
+  for (int64_t batch = static_cast<int64_t>(blockIdx.x) * kRouteWaves + wv; batch * kTokens < a.tokens; batch += step) {
+    const int64_t t = batch * kTokens + tl;
+    const bool there = t < a.tokens;
+    int32_t e[MM];
+    float g[MM], l[MM];
+#pragma unroll
+    for (int mm = 0; mm < MM; ++mm) {
+      const int j = mm * LPT + q;
+      e[mm] = there && j < a.k ? topk_idx[t * a.k + j] : -1;
+      g[mm] = there && j < a.k ? grad_w[t * a.k + j] : 0.f;
+    }
+#pragma unroll
+    for (int mm = 0; mm < MM; ++mm) {
+      if (e[mm] >= E) e[mm] = -1;
+      l[mm] = e[mm] >= 0 ? load_logit(a, t * E + e[mm]) : 0.f;
+      if (masked(l[mm])) e[mm] = -1;
+    }
+    // is an id there twice?  Each writes its place and looks whether it is still there.
+#pragma unroll
+    for (int mm = 0; mm < MM; ++mm)
+      if (e[mm] >= 0) reinterpret_cast<int32_t*>(row)[e[mm]] = mm * LPT + q;
+    wave_sync();
+    bool twice = false;
+#pragma unroll
+    for (int mm = 0; mm < MM; ++mm)
+      if (e[mm] >= 0) twice |= reinterpret_cast<int32_t*>(row)[e[mm]] != mm * LPT + q;
+    wave_sync();
+    // scores and weights
+    float d[MM], total = 0.f, inv = 0.f;
     if (every) {
+      float m = -__builtin_huge_valf(), sum = 0.f;
+      for (int i = 4 * q; i < E; i += 4 * LPT) {
+        f32x4 x;
+        if (logits_in_fours) {
+          if (a.bf16) {
+            const u32x2 v = there ? *reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(a.logits) + t * E + i) : u32x2{0, 0};
+            x = f32x4{bf16_lo(v[0]), bf16_hi(v[0]), bf16_lo(v[1]), bf16_hi(v[1])};
+          } else {
+            x = there ? *reinterpret_cast<const f32x4*>(static_cast<const float*>(a.logits) + t * E + i) : f32x4{0.f, 0.f, 0.f, 0.f};
+          }
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int e = lane + 64 * v;
-        l[v] = e < a.E ? load_logit(a, t * a.E + e) : -__builtin_huge_valf();
+          for (int c = 0; c < 4; ++c) x[c] = clean_logit(x[c]);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) x[c] = !there ? 0.f : i + c < E ? load_logit(a, t * E + i + c) : -__builtin_huge_valf();
+        }
+        *reinterpret_cast<f32x4*>(row + i) = x;
+        m = fmaxf(m, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
       }
-      soft = soft_of(a, t);
-    }
-    int32_t e_j = lane < a.k ? topk_idx[t * a.k + lane] : -1;
-    if (e_j < 0 || e_j >= a.E) e_j = -1;
-    const float l_j = e_j >= 0 ? load_logit(a, t * a.E + e_j) : -__builtin_huge_valf();
-    if (masked(l_j)) e_j = -1;
-    const bool some = e_j >= 0;
-    const double g = some ? static_cast<double>(grad_w[t * a.k + lane]) : 0.0;
-    const double s = score_of(a.sigmoid, l_j, soft);
-    const double w = weight_of(a, some, some ? l_j : 0.f, s);
-    const double total = wave_sum_f64(w * g);
-    double d = a.renorm ? w * (g - total / a.scale) : w * g;
-    if (a.sigmoid) d *= 1.0 - s;
-    if (!some) d = 0.0;
-    const float df = static_cast<float>(d);
-    float out[V];
+      m = token_max<LPT>(m);
+      if (masked(m)) m = 0.f;  // all of them
+      for (int i = 4 * q; i < E; i += 4 * LPT) {
+        f32x4 x = *reinterpret_cast<const f32x4*>(row + i);
 #pragma unroll
-    for (int v = 0; v < V; ++v) out[v] = every && !masked(l[v]) ? static_cast<float>(-total * score_of(false, l[v], soft)) : 0.f;
-    for (int j = 0; j < a.k; ++j) {
-      const int32_t e = static_cast<int32_t>(readlane(static_cast<uint32_t>(e_j), j));
-      const float x = readlane_f(df, j);
+        for (int c = 0; c < 4; ++c) x[c] = __builtin_amdgcn_exp2f((x[c] - m) * kLog2e);
+        *reinterpret_cast<f32x4*>(row + i) = x;
+        sum += (x[0] + x[1]) + (x[2] + x[3]);
+      }
+      sum = token_sum<LPT>(sum);
+      inv = sum > 0.f ? 1.f / sum : 0.f;
+      wave_sync();
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (lane + 64 * v == e) out[v] += x;
-    }
+      for (int mm = 0; mm < MM; ++mm) {
+        d[mm] = e[mm] >= 0 ? a.scale * (row[e[mm]] * inv) * g[mm] : 0.f;
+        total += d[mm];
+      }
+      total = token_sum<LPT>(total);
+      wave_sync();
+      const float each = -inv * total;
+      for (int i = 4 * q; i < E; i += 4 * LPT) *reinterpret_cast<f32x4*>(row + i) *= each;
+    } else {
+      float m = -__builtin_huge_valf(), sum = 0.f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int e = lane + 64 * v;
-      if (e >= a.E) continue;
-      if (a.bf16)
-        static_cast<uint16_t*>(grad_logits)[t * a.E + e] = static_cast<uint16_t>(pack_bf16(out[v], 0.f));
-      else
-        static_cast<float*>(grad_logits)[t * a.E + e] = out[v];
+      for (int mm = 0; mm < MM; ++mm)
+        if (e[mm] >= 0) m = fmaxf(m, l[mm]);
+      m = token_max<LPT>(m);
+      if (a.sigmoid) m = a.renorm ? fminf(m, 0.f) : 0.f;
+      const float over = a.sigmoid ? expf(-m) : 1.f;
+      float rest[MM], w[MM];
+#pragma unroll
+      for (int mm = 0; mm < MM; ++mm) {
+        const float x = expf(a.sigmoid ? -fabsf(l[mm]) : l[mm] - m), big = 1.f / (1.f + x);
+        rest[mm] = l[mm] > 0.f ? x * big : big;  // 1 - s
+        w[mm] = a.sigmoid ? (l[mm] > 0.f ? over : expf(l[mm] - m)) * big : x;
+        if (e[mm] < 0) w[mm] = 0.f;
+        sum += w[mm];
+      }
+      const float factor = a.scale * (a.renorm ? 1.f / token_sum<LPT>(sum) : 1.f);
+#pragma unroll
+      for (int mm = 0; mm < MM; ++mm) {
+        if (e[mm] < 0) continue;
+        w[mm] *= factor;
+        total += w[mm] * g[mm];
+      }
+      // the sum without the scale, which may be zero
+      total = a.renorm ? token_sum<LPT>(total) : 0.f;
+      const float back = a.renorm && a.scale != 0.f ? total / a.scale : 0.f;
+#pragma unroll
+      for (int mm = 0; mm < MM; ++mm) {
+        d[mm] = w[mm] * (g[mm] - back);
+        if (a.sigmoid) d[mm] *= rest[mm];
+      }
+      const u32x4 zero = {0, 0, 0, 0};
+      for (int i = 4 * lane; i < words; i += 256) *reinterpret_cast<u32x4*>(rows + i) = zero;
     }
+    if (__builtin_expect(ballot(twice) != 0, 0)) merge_same<LPT, MM>(e, d);
+    wave_sync();
+#pragma unroll
+    for (int mm = 0; mm < MM; ++mm)
+      if (e[mm] >= 0) row[e[mm]] = every ? row[e[mm]] + d[mm] : d[mm];
+    wave_sync();
+    // out, all rows of the wave as one range
+    const int32_t values = static_cast<int32_t>(min(a.tokens - batch * kTokens, static_cast<int64_t>(kTokens))) * E;
+    char* out = static_cast<char*>(grad_logits) + batch * kTokens * E * (a.bf16 ? 2 : 4);
+    if (in_fours) {
+      for (int i = 4 * lane; i < values; i += 256) {
+        const int r = static_cast<int>((static_cast<float>(i) + 0.5f) * per_row);
+        const f32x4 x = *reinterpret_cast<const f32x4*>(rows + i + r * (pitch - E));
+        if (a.bf16) {
+          const u32x2 y = {pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
+          *reinterpret_cast<u32x2*>(out + 2 * i) = y;
+        } else {
+          *reinterpret_cast<f32x4*>(out + 4 * i) = x;
+        }
+      }
+    } else {
+      for (int i = lane; i < values; i += 64) {
+        const int r = static_cast<int>((static_cast<float>(i) + 0.5f) * per_row);
+        const float x = rows[i + r * (pitch - E)];
+        if (a.bf16)
+          reinterpret_cast<uint16_t*>(out)[i] = static_cast<uint16_t>(pack_bf16(x, 0.f));
+        else
+          reinterpret_cast<float*>(out)[i] = x;
+      }
+    }
+    wave_sync();
   }
 }
 
@@ -747,16 +880,29 @@ hipError_t launch_route(const RouteArgs& args, int32_t* idx, float* w, hipStream
   return hipGetLastError();
 }
 
+namespace {
+
+template <int LPT, int MM>
+void launch_backward_as(const RouteArgs& a, const int32_t* idx, const float* grad_w, void* grad_logits, hipStream_t st) {
+  const size_t lds = kRouteWaves * grad_words<LPT>(a.E) * sizeof(float);
+  const int64_t want = (a.tokens + 64 / LPT * kRouteWaves - 1) / (64 / LPT * kRouteWaves), most = 1024;
+  hipLaunchKernelGGL((route_backward_kernel<LPT, MM>), dim3(static_cast<uint32_t>(want < most ? want : most)), dim3(kRouteThreads), lds, st,
+                     a, idx, grad_w, grad_logits);
+}
+
+template <int LPT>
+void launch_backward_of(const RouteArgs& a, const int32_t* idx, const float* grad_w, void* grad_logits, hipStream_t st) {
+  const auto go = a.k <= LPT ? launch_backward_as<LPT, 1> : a.k <= 2 * LPT ? launch_backward_as<LPT, 2> : launch_backward_as<LPT, 64 / LPT>;
+  go(a, idx, grad_w, grad_logits, st);
+}
+
+}  // namespace
+
 hipError_t launch_route_backward(const RouteArgs& a, const int32_t* idx, const float* grad_w, void* grad_logits,
                                  hipStream_t st) {
   if (a.tokens == 0) return hipSuccess;
-  const dim3 grid(route_grid(a.tokens)), block(kRouteThreads);
-  if (a.E <= 64)
-    hipLaunchKernelGGL(route_backward_kernel<1>, grid, block, 0, st, a, idx, grad_w, grad_logits);
-  else if (a.E <= 256)
-    hipLaunchKernelGGL(route_backward_kernel<4>, grid, block, 0, st, a, idx, grad_w, grad_logits);
-  else
-    hipLaunchKernelGGL(route_backward_kernel<16>, grid, block, 0, st, a, idx, grad_w, grad_logits);
+  const auto go = a.E <= 256 ? launch_backward_of<8> : launch_backward_of<16>;
+  go(a, idx, grad_w, grad_logits, st);
   return hipGetLastError();
 }
 
