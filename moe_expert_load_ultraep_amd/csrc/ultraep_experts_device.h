@@ -161,9 +161,8 @@ __device__ __forceinline__ u32x2 to_e4m3(const u32x4& x, float scale) {
 // The same from fp32 values: magnitudes as fp32 bits.
 constexpr uint32_t kNotFiniteF32 = 0x7F800000;
 
-__device__ __forceinline__ uint32_t magnitude(float v) { return __builtin_bit_cast(uint32_t, v) & 0x7FFFFFFFu; }
 __device__ __forceinline__ uint32_t finite_magnitude(float v) {
-  const uint32_t m = magnitude(v);
+  const uint32_t m = __builtin_bit_cast(uint32_t, v) & 0x7FFFFFFFu;
   return m < kNotFiniteF32 ? m : 0u;
 }
 
@@ -172,18 +171,26 @@ __device__ __forceinline__ int32_t block_exponent_f32(uint32_t amax) {
   return amax == 0 ? 0 : max(e, -126);
 }
 
-// Largest finite magnitude of the 16 lanes' values, as fp32 bits, in every lane.
-__device__ __forceinline__ uint32_t row16_amax(const float (&x)[8]) {
+// Largest magnitude of N values but for NaN, as fp32 bits; infinite
+// ones are left out only where FINITE.
+template <bool FINITE, int N>
+__device__ __forceinline__ uint32_t amax_of(const float (&x)[N]) {
+  if (!FINITE) {
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) m = fmaxf(m, fabsf(x[i]));
+    return __builtin_bit_cast(uint32_t, m);
+  }
   uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, magnitude(x[i]));
-  m = row16_max(m);
-  if (__builtin_expect(ballot(m >= kNotFiniteF32) != 0, 0)) {
-    m = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, finite_magnitude(x[i]));
-    m = row16_max(m);
-  }
+  for (int i = 0; i < N; ++i) m = max(m, finite_magnitude(x[i]));
+  return m;
+}
+
+// Largest finite magnitude of the 16 lanes' values, as fp32 bits, in every lane.
+__device__ __forceinline__ uint32_t row16_amax(const float (&x)[8]) {
+  const uint32_t m = row16_max(amax_of<false>(x));
+  if (__builtin_expect(ballot(m >= kNotFiniteF32) != 0, 0)) return row16_max(amax_of<true>(x));
   return m;
 }
 
@@ -204,24 +211,6 @@ __device__ __forceinline__ uint32_t four_scales(int32_t e) {
 #pragma unroll
   for (int b = 0; b < 4; ++b) s |= (readlane(static_cast<uint32_t>(e), 16 * b) + 127u) << (8 * b);
   return s;
-}
-
-// 128 x 128 tiles, transposed on their way out.  A thread holds 8 x 8 values:
-// row group g = thread / 16 (rows 8g..8g+7), column group c = thread % 16.
-// Bytes wait in LDS as [column][row] with the 8-byte row groups of a column
-// exchanged by g ^ (column / 8), so that neither the stores (16 column groups
-// at once) nor the reads have bank conflicts.
-__device__ __forceinline__ void put_column_bytes(uint8_t* tile, int c, int g, const u32x2 (&b)[8]) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    *reinterpret_cast<u32x2*>(tile + (8 * c + j) * kQBlock + ((g ^ c) & 15) * 8) = b[j];
-}
-
-// 16 rows (r0 = 16 * part) of column h.
-__device__ __forceinline__ u32x4 get_column_bytes(const uint8_t* tile, int h, int part) {
-  const int c = (h >> 3) & 15;
-  const u32x4 v = *reinterpret_cast<const u32x4*>(tile + h * kQBlock + (((2 * part) ^ (c & 14)) * 8));
-  return (c & 1) ? u32x4{v[2], v[3], v[0], v[1]} : v;
 }
 
 }  // namespace

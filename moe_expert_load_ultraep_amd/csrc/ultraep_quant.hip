@@ -66,6 +66,24 @@ __global__ __launch_bounds__(kQuantThreads) void quant_rows_kernel(
   }
 }
 
+// 128 x 128 tiles, transposed on their way out.  A thread holds 8 x 8 values:
+// row group g = thread / 16 (rows 8g..8g+7), column group c = thread % 16.
+// Bytes wait in LDS as [column][row] with the 8-byte row groups of a column
+// exchanged by g ^ (column / 8), so that neither the stores (16 column groups
+// at once) nor the reads have bank conflicts.
+__device__ __forceinline__ void put_column_bytes(uint8_t* tile, int c, int g, const u32x2 (&b)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    *reinterpret_cast<u32x2*>(tile + (8 * c + j) * kQBlock + ((g ^ c) & 15) * 8) = b[j];
+}
+
+// 16 rows (r0 = 16 * part) of column h.
+__device__ __forceinline__ u32x4 get_column_bytes(const uint8_t* tile, int h, int part) {
+  const int c = (h >> 3) & 15;
+  const u32x4 v = *reinterpret_cast<const u32x4*>(tile + h * kQBlock + (((2 * part) ^ (c & 14)) * 8));
+  return (c & 1) ? u32x4{v[2], v[3], v[0], v[1]} : v;
+}
+
 // 8 x 8 transpose of bytes: b[j] holds column j's rows from a's rows.
 __device__ __forceinline__ void transpose_bytes(const u32x2 (&a)[8], u32x2 (&b)[8]) {
 #pragma unroll
