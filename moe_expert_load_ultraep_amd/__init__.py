@@ -135,13 +135,14 @@ def _check(fn: str, status: int) -> None:
         raise UltraEPError(fn, status)
 
 
-def _stream(stream) -> Optional[int]:
+def _stream(stream, dev: Optional[int] = None) -> Optional[int]:
+    """The handle of a given stream, or of the current one (of device `dev`, the current one)."""
     if stream is not None:
         return int(stream) if isinstance(stream, int) else stream.cuda_stream
     import torch
     # the current stream's handle without building a Stream object (2.7 us of a 5 us call); not a public call
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
+    return raw(torch.cuda.current_device() if dev is None else dev) if raw else torch.cuda.current_stream().cuda_stream
 
 
 def _ptr(t) -> Optional[int]:
@@ -316,16 +317,16 @@ def pointer_table(tensors, device="cuda"):
     return torch.tensor([0 if t is None else t.data_ptr() for t in tensors], dtype=torch.int64).to(device)
 
 
-_BYTES = _HALVES = _LONGS = _INTS = _FLOATS = _device = None
+_BYTES = _HALVES = _LONGS = _INTS = _FLOATS = _BF16 = _device = None
 
 
 def _types():
     """The types a call's buffers may have, and the current device's index, found once torch is in use."""
-    global _BYTES, _HALVES, _LONGS, _INTS, _FLOATS, _device
+    global _BYTES, _HALVES, _LONGS, _INTS, _FLOATS, _BF16, _device
     import torch
     _BYTES = (torch.uint8, torch.float8_e4m3fn)
     _HALVES = (torch.bfloat16, torch.int16, torch.uint16)
-    _LONGS, _INTS, _FLOATS = (torch.int64,), (torch.int32,), (torch.float32,)
+    _LONGS, _INTS, _FLOATS, _BF16 = (torch.int64,), (torch.int32,), (torch.float32,), (torch.bfloat16,)
     _device = lambda: torch.cuda.current_device() if torch.cuda.is_initialized() else None  # noqa: E731
 
 
@@ -468,20 +469,34 @@ def ultraep_grad_clip(ctx: Context, tensors, numels, n: int, dtype, sumsq, max_n
     _check(fn, st)
 
 
-# The steps around the experts, with the same checks.
-def _type_code(fn: str, t) -> int:
-    """The code of a buffer's type, fp32 or bf16."""
-    import torch
-    _need(fn, t is not None and (t.dtype is torch.float32 or t.dtype is torch.bfloat16))
-    return int(t.dtype is torch.bfloat16)
+# The steps around the experts, with the same checks; a serving step's calls wait for
+# them, so each tensor is looked at once.
+def _fits(t, dev, dtypes, shape) -> bool:
+    """_is for a given whole shape."""
+    return t.dtype in dtypes and t.shape == shape and t.get_device() == dev and t.is_contiguous()
 
 
-def _route_checks(fn: str, ctx, dev, logits, k: int, topk_idx, w) -> tuple:
+def _or_none(t, dev, dtypes, shape) -> bool:
+    return t is None or (t.dtype in dtypes and t.shape == shape and t.get_device() == dev and t.is_contiguous())
+
+
+def _type_code(fn: str, t) -> tuple:
+    """The code and the type of a buffer, fp32 or bf16."""
+    if t is not None:
+        if t.dtype is _BF16[0]:
+            return 1, _BF16
+        if t.dtype is _FLOATS[0]:
+            return 0, _FLOATS
+    raise UltraEPError(fn, -1)
+
+
+def _route_checks(fn: str, ctx, dev, logits, k: int, topk_idx, w, grad_logits=None) -> tuple:
     """(tokens, type code) of a routing call."""
-    code = _type_code(fn, logits)
-    _need(fn, _is(logits, dev, (logits.dtype,), None, ctx.E))
-    n = logits.shape[0]
-    _need(fn, _is(topk_idx, dev, _INTS, n, k) and _is(w, dev, _FLOATS, n, k))
+    code, own = _type_code(fn, logits)
+    _need(fn, logits.dim() == 2)
+    n, E = logits.shape
+    _need(fn, E == ctx.E and logits.get_device() == dev and logits.is_contiguous() and topk_idx is not None and w is not None
+          and _fits(topk_idx, dev, _INTS, (n, k)) and _fits(w, dev, _FLOATS, (n, k)) and _or_none(grad_logits, dev, own, (n, E)))
     return n, code
 
 
@@ -495,9 +510,9 @@ def ultraep_route(ctx: Context, logits, k: int, topk_idx, topk_w, score: int = R
     fn = "ultraep_route"
     dev = _here()
     n, code = _route_checks(fn, ctx, dev, logits, k, topk_idx, topk_w)
-    _need(fn, bias is None or _is(bias, dev, _FLOATS, ctx.E))
-    st = lib().ultraep_route(ctx.handle, _ptr(logits), code, n, k, score, _ptr(bias), groups, topk_groups, group_top,
-                             int(renormalize), scale, _ptr(topk_idx), _ptr(topk_w), _stream(stream))
+    _need(fn, _or_none(bias, dev, _FLOATS, (ctx.E,)))
+    st = lib().ultraep_route(ctx.handle, logits.data_ptr(), code, n, k, score, _ptr(bias), groups, topk_groups, group_top,
+                             int(renormalize), scale, topk_idx.data_ptr(), topk_w.data_ptr(), _stream(stream, dev))
     _check(fn, st)
 
 
@@ -506,10 +521,11 @@ def ultraep_route_backward(ctx: Context, logits, k: int, topk_idx, grad_topk_w, 
     """grad_logits [tokens, E] (the logits' type) from the gradients of ultraep_route's weights."""
     fn = "ultraep_route_backward"
     dev = _here()
-    n, code = _route_checks(fn, ctx, dev, logits, k, topk_idx, grad_topk_w)
-    _need(fn, _is(grad_logits, dev, (logits.dtype,), n, ctx.E))
-    st = lib().ultraep_route_backward(ctx.handle, _ptr(logits), code, n, k, score, int(renormalize), scale, _ptr(topk_idx),
-                                      _ptr(grad_topk_w), _ptr(grad_logits), _stream(stream))
+    _need(fn, grad_logits is not None)
+    n, code = _route_checks(fn, ctx, dev, logits, k, topk_idx, grad_topk_w, grad_logits)
+    st = lib().ultraep_route_backward(ctx.handle, logits.data_ptr(), code, n, k, score, int(renormalize), scale,
+                                      topk_idx.data_ptr(), grad_topk_w.data_ptr(), grad_logits.data_ptr(),
+                                      _stream(stream, dev))
     _check(fn, st)
 
 
@@ -522,17 +538,16 @@ def ultraep_residual_norm(ctx: Context, x, weight, eps: float, residual=None, h=
     rstd fp32 [rows].  Outputs that are not wanted are None."""
     fn = "ultraep_residual_norm"
     dev = _here()
-    _need(fn, x is not None and x.dim() == 2 and (q is None) == (q_scale is None))
-    n, H = x.shape
-    w_code, r_code = _type_code(fn, weight), 1 if residual is None else _type_code(fn, residual)
-    _need(fn, _is(x, dev, _HALVES, n, H) and _is(weight, dev, (weight.dtype,), H)
-          and (residual is None or _is(residual, dev, (residual.dtype,), n, H))
-          and (h is None or (residual is not None and _is(h, dev, (residual.dtype,), n, H)))
-          and (y is None or _is(y, dev, _HALVES, n, H))
-          and (q is None or (_is(q, dev, _BYTES, n, quant_pitch(H)) and _is(q_scale, dev, _BYTES, n, quant_scale_pitch(H))))
-          and (rstd is None or _is(rstd, dev, _FLOATS, n)))
-    st = lib().ultraep_residual_norm(ctx.handle, _ptr(x), _ptr(residual), r_code, _ptr(weight), w_code, eps, n, H, _ptr(h),
-                                     _ptr(y), _ptr(q), _ptr(q_scale), _ptr(rstd), _stream(stream))
+    _need(fn, x is not None and x.dim() == 2 and (q is None) == (q_scale is None) and (h is None or residual is not None))
+    shape = x.shape
+    n, H = shape
+    w_code, w_type = _type_code(fn, weight)
+    r_code, r_type = (1, _BF16) if residual is None else _type_code(fn, residual)
+    _need(fn, _fits(x, dev, _HALVES, shape) and _fits(weight, dev, w_type, (H,)) and _or_none(residual, dev, r_type, shape)
+          and _or_none(h, dev, r_type, shape) and _or_none(y, dev, _HALVES, shape) and _or_none(rstd, dev, _FLOATS, (n,))
+          and (q is None or (_fits(q, dev, _BYTES, (n, quant_pitch(H))) and _fits(q_scale, dev, _BYTES, (n, quant_scale_pitch(H))))))
+    st = lib().ultraep_residual_norm(ctx.handle, x.data_ptr(), _ptr(residual), r_code, weight.data_ptr(), w_code, eps, n, H,
+                                     _ptr(h), _ptr(y), _ptr(q), _ptr(q_scale), _ptr(rstd), _stream(stream, dev))
     _check(fn, st)
 
 
@@ -552,33 +567,36 @@ def ultraep_residual_norm_backward(ctx: Context, grad_y, h, weight, rstd, grad_h
     residual_norm_workspace_bytes(rows, H)."""
     fn = "ultraep_residual_norm_backward"
     dev = _here()
-    _need(fn, h is not None and h.dim() == 2)
-    n, H = h.shape
-    w_code, h_code = _type_code(fn, weight), _type_code(fn, h)
-    own = (h.dtype,)
-    _need(fn, _is(h, dev, own, n, H) and _is(grad_y, dev, _HALVES, n, H) and _is(weight, dev, (weight.dtype,), H)
-          and _is(rstd, dev, _FLOATS, n) and _is(grad_h, dev, own, n, H) and (grad_in is None or _is(grad_in, dev, own, n, H))
-          and (grad_x is None or _is(grad_x, dev, _HALVES, n, H)) and (grad_weight is None or _is(grad_weight, dev, _FLOATS, H))
+    _need(fn, h is not None and h.dim() == 2 and grad_y is not None and rstd is not None and grad_h is not None)
+    shape = h.shape
+    n, H = shape
+    w_code, w_type = _type_code(fn, weight)
+    h_code, own = _type_code(fn, h)
+    _need(fn, _fits(h, dev, own, shape) and _fits(grad_y, dev, _HALVES, shape) and _fits(weight, dev, w_type, (H,))
+          and _fits(rstd, dev, _FLOATS, (n,)) and _fits(grad_h, dev, own, shape) and _or_none(grad_in, dev, own, shape)
+          and _or_none(grad_x, dev, _HALVES, shape) and _or_none(grad_weight, dev, _FLOATS, (H,))
           and (workspace is None or (workspace.get_device() == dev and workspace.is_contiguous())))
-    st = lib().ultraep_residual_norm_backward(ctx.handle, _ptr(grad_y), _ptr(h), h_code, _ptr(weight), w_code, _ptr(rstd),
-                                              _ptr(grad_in), n, H, _ptr(grad_h), _ptr(grad_x), _ptr(grad_weight),
-                                              int(accumulate), _ptr(workspace),
+    st = lib().ultraep_residual_norm_backward(ctx.handle, grad_y.data_ptr(), h.data_ptr(), h_code, weight.data_ptr(), w_code,
+                                              rstd.data_ptr(), _ptr(grad_in), n, H, grad_h.data_ptr(), _ptr(grad_x),
+                                              _ptr(grad_weight), int(accumulate), _ptr(workspace),
                                               0 if workspace is None else workspace.numel() * workspace.element_size(),
-                                              _stream(stream))
+                                              _stream(stream, dev))
     _check(fn, st)
 
 
 def _glu_checks(fn: str, ctx, dev, plan, h, W: int, q, q_scale, qt, qt_scale, rows: int) -> int:
     """Blocks of the columns form of a gated activation's results, W columns."""
     _need(fn, (q is None) == (q_scale is None) and (qt is None) == (qt_scale is None) and not (q is None and qt is None)
-          and _is_plan(ctx, plan, dev) and 0 <= rows <= h.shape[0] and _is(h, dev, _HALVES, None, h.shape[1]))
+          and _is_plan(ctx, plan, dev) and 0 <= rows <= h.shape[0] and h.dtype in _HALVES and h.get_device() == dev
+          and h.is_contiguous())
     if q is not None:
-        _need(fn, _is(q, dev, _BYTES, None, quant_pitch(W)) and _is(q_scale, dev, _BYTES, q.shape[0], quant_scale_pitch(W))
-              and rows <= q.shape[0])
+        n = q.shape[0]
+        _need(fn, rows <= n and _fits(q, dev, _BYTES, (n, quant_pitch(W))) and _fits(q_scale, dev, _BYTES, (n, quant_scale_pitch(W))))
     if qt is None:
         return 0
-    _need(fn, _is(qt, dev, _BYTES, None, W, QUANT_BLOCK) and _is(qt_scale, dev, _BYTES, qt.shape[0], W))
-    return qt.shape[0]
+    blocks = qt.shape[0]
+    _need(fn, _fits(qt, dev, _BYTES, (blocks, W, QUANT_BLOCK)) and _fits(qt_scale, dev, _BYTES, (blocks, W)))
+    return blocks
 
 
 def ultraep_glu_quant(ctx: Context, plan, h, p_begin: int, p_end: int, q=None, q_scale=None, qt=None, qt_scale=None,
@@ -590,12 +608,13 @@ def ultraep_glu_quant(ctx: Context, plan, h, p_begin: int, p_end: int, q=None, q
     fn = "ultraep_glu_quant"
     dev = _here()
     _need(fn, h is not None and h.dim() == 2 and h.shape[1] % 2 == 0)
-    F = h.shape[1] // 2
+    n, F = h.shape
+    F //= 2
     if rows is None:
-        rows = h.shape[0]
+        rows = n
     blocks = _glu_checks(fn, ctx, dev, plan, h, F, q, q_scale, qt, qt_scale, rows)
-    st = lib().ultraep_glu_quant(ctx.handle, _ptr(plan), _ptr(h), F, activation, p_begin, p_end, _ptr(q), _ptr(q_scale),
-                                 _ptr(qt), _ptr(qt_scale), rows, blocks, _stream(stream))
+    st = lib().ultraep_glu_quant(ctx.handle, plan.data_ptr(), h.data_ptr(), F, activation, p_begin, p_end, _ptr(q),
+                                 _ptr(q_scale), _ptr(qt), _ptr(qt_scale), rows, blocks, _stream(stream, dev))
     _check(fn, st)
 
 
@@ -605,14 +624,15 @@ def ultraep_glu_quant_backward(ctx: Context, plan, h, grad, p_begin: int, p_end:
     [., quant_pitch(2F)], qt [blocks, 2F, 128] and their scales."""
     fn = "ultraep_glu_quant_backward"
     dev = _here()
-    _need(fn, h is not None and h.dim() == 2 and h.shape[1] % 2 == 0)
-    W = h.shape[1]
+    _need(fn, h is not None and h.dim() == 2 and h.shape[1] % 2 == 0 and grad is not None and grad.dim() == 2)
+    n, W = h.shape
     if rows is None:
-        rows = h.shape[0]
+        rows = n
     blocks = _glu_checks(fn, ctx, dev, plan, h, W, q, q_scale, qt, qt_scale, rows)
-    _need(fn, _is(grad, dev, _HALVES, None, W // 2) and rows <= grad.shape[0])
-    st = lib().ultraep_glu_quant_backward(ctx.handle, _ptr(plan), _ptr(h), _ptr(grad), W // 2, activation, p_begin, p_end,
-                                          _ptr(q), _ptr(q_scale), _ptr(qt), _ptr(qt_scale), rows, blocks, _stream(stream))
+    _need(fn, _fits(grad, dev, _HALVES, (grad.shape[0], W // 2)) and rows <= grad.shape[0])
+    st = lib().ultraep_glu_quant_backward(ctx.handle, plan.data_ptr(), h.data_ptr(), grad.data_ptr(), W // 2, activation,
+                                          p_begin, p_end, _ptr(q), _ptr(q_scale), _ptr(qt), _ptr(qt_scale), rows, blocks,
+                                          _stream(stream, dev))
     _check(fn, st)
 
 
