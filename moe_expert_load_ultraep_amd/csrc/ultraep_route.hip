@@ -169,9 +169,9 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a, int32
 // nothing has to be looked up afterwards.  Where two keys that the choice or its order
 // hangs on are nearer than their errors can be, the token is done again in fp64
 // (route_token), so the ids are always those of fp64.
-template <int LPT>
+template <int LPT, int NI>
 struct Packed {
-  static constexpr int kIdBits = LPT == 4 ? 8 : 9;
+  static constexpr int kIdBits = LPT * NI * 4 <= 256 ? 8 : 9;
   static constexpr uint32_t kIds = (1u << kIdBits) - 1;
   static constexpr float kTop = static_cast<float>(1u << (32 - kIdBits));  // values are below
 };
@@ -274,7 +274,7 @@ __device__ __forceinline__ KeyUnits bias_units(const RouteArgs& a, float* table)
     hi = fmaxf(hi, s_hi[i]);
   }
   const float span = hi - lo + 1.f;
-  KeyUnits u{(Packed<LPT>::kTop - 64.f) / span, !(span < 1e4f)};
+  KeyUnits u{(Packed<LPT, NI>::kTop - 64.f) / span, !(span < 1e4f)};
   for (int e = tid; e < kAll; e += kRouteThreads) {
     const float b = e < a.E ? a.bias[e] : __builtin_nanf("");
     table[e] = b > -__builtin_huge_valf() ? (b - lo) * u.c + 8.f : __builtin_nanf("");
@@ -293,7 +293,7 @@ template <int LPT, int NI, int KL>
 __global__ __launch_bounds__(kRouteThreads, NI > 10 ? 3 : 4) void route_fast_kernel(RouteArgs a, int32_t* __restrict__ topk_idx,
                                                                    float* __restrict__ topk_w) {
   extern __shared__ __align__(16) char s_dyn[];
-  using P = Packed<LPT>;
+  using P = Packed<LPT, NI>;
   constexpr int kTokens = 64 / LPT, kAll = LPT * NI * 4, MM = (KL - 1 + LPT - 1) / LPT;
   constexpr float kHigh = P::kTop - 64.f, kPerLogit = kHigh / kLogitRange;
   const int wv = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
@@ -306,7 +306,7 @@ __global__ __launch_bounds__(kRouteThreads, NI > 10 ? 3 : 4) void route_fast_ker
   KeyUnits units{0.f, false};
   if (with_bias) units = bias_units<LPT, NI>(a, bias);
   // what two keys have to be apart for their order to be certain, in units
-  const uint32_t margin = with_bias ? (a.sigmoid ? (LPT == 4 ? 13u : 9u) : (LPT == 4 ? 64u : 40u)) : a.bf16 ? 0u : 8u;
+  const uint32_t margin = with_bias ? (a.sigmoid ? (P::kIdBits == 8 ? 13u : 9u) : (P::kIdBits == 8 ? 64u : 40u)) : a.bf16 ? 0u : 8u;
   const int64_t step = static_cast<int64_t>(gridDim.x) * kRouteWaves;
   float l[4 * NI];
   // A batch's logits through one resource: an address a lane, chunks at constant
@@ -445,7 +445,7 @@ __global__ __launch_bounds__(kRouteThreads, NI > 10 ? 3 : 4) void route_fast_ker
     load(batch + step, lane, E);  // the next round's, on their way while this one's are chosen
     if (a.groups > 1) {
       wave_sync();
-      constexpr int kOwn = kFastGroups / LPT;
+      constexpr int kOwn = (kFastGroups + LPT - 1) / LPT;
       float worth[kOwn];
       const uint32_t* row = keys + tl * pitch;
 #pragma unroll
@@ -865,14 +865,22 @@ hipError_t launch_route(const RouteArgs& args, int32_t* idx, float* w, hipStream
   RouteArgs a = args;
   if (a.topk_groups == a.groups) a.groups = a.topk_groups = 1;  // all of them stay
   if (fast_route(a)) {
-    const auto go = a.E <= 32    ? launch_fast_of<4, 2>
+    // Few tokens: more lanes for each, whose work is done sooner (1024 of 256 experts in
+    // groups: 16 lanes 8.5 us, 8 9.3, 4 12.5; 8192: 16.8, 16.3, 19.6).  Many: fewer, which
+    // merge less; but with groups of many experts their keys fill LDS, and smaller rounds let
+    // more waves in (262144 tokens of 256 experts: 8 lanes 104 us, 4 108; of 128 in groups
+    // 65536: 26 and 24; 524288 of 128 without groups: 98 and 84).
+    const int lanes = a.E > 256 ? 8 : a.tokens <= 4096 ? 16 : a.tokens <= 16384 || (a.groups > 1 && a.E > 128) ? 8 : 4;
+    const auto go = lanes == 16  ? (a.E <= 128 ? launch_fast_of<16, 2> : launch_fast_of<16, 4>)
+                    : lanes == 8 ? (a.E <= 128   ? launch_fast_of<8, 4>
+                                    : a.E <= 256 ? launch_fast_of<8, 8>
+                                    : a.E <= 384 ? launch_fast_of<8, 12>
+                                                 : launch_fast_of<8, 16>)
+                    : a.E <= 32  ? launch_fast_of<4, 2>
                     : a.E <= 64  ? launch_fast_of<4, 4>
                     : a.E <= 128 ? launch_fast_of<4, 8>
                     : a.E <= 160 ? launch_fast_of<4, 10>
-                    : a.E <= 192 ? launch_fast_of<4, 12>
-                    : a.E <= 256 ? launch_fast_of<4, 16>
-                    : a.E <= 384 ? launch_fast_of<8, 12>
-                                 : launch_fast_of<8, 16>;
+                                 : launch_fast_of<4, 16>;
     go(a, idx, w, st);
     return hipGetLastError();
   }
