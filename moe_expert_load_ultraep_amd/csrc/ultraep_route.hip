@@ -283,6 +283,24 @@ __device__ __forceinline__ KeyUnits bias_units(const RouteArgs& a, float* table)
   return u;
 }
 
+// Key of e0 less that of e1 in fp64, for the token whose logits start at `row`.  A softmax
+// is taken by its sum in fp32 (inv, its inverse), off by less than 2^-19: where that could
+// decide, the answer is not sure.
+__device__ __forceinline__ double exact_difference(const RouteArgs& a, int64_t row, int32_t e0, int32_t e1, float top, float inv,
+                                                   bool& sure) {
+  const double l0 = static_cast<double>(load_logit(a, row + e0)), l1 = static_cast<double>(load_logit(a, row + e1));
+  if (a.bias == nullptr) return l0 - l1;
+  const double b = static_cast<double>(a.bias[e0]) - static_cast<double>(a.bias[e1]);
+  if (a.sigmoid) {  // as the definition adds them, so that equal ones are equal
+    const double k0 = score_of(true, static_cast<float>(l0), Soft{}) + static_cast<double>(a.bias[e0]);
+    const double k1 = score_of(true, static_cast<float>(l1), Soft{}) + static_cast<double>(a.bias[e1]);
+    return k0 - k1;
+  }
+  const double s = (exp(l0 - top) - exp(l1 - top)) * inv, d = s + b;
+  sure = fabs(d) > fabs(s) * 0x1p-19 + 0x1p-40;
+  return d;
+}
+
 // Words of LDS a wave has for itself: keys and worths of its tokens' groups, or E fp64.
 template <int LPT>
 __host__ __device__ inline int32_t wave_words(const RouteArgs& a) {
@@ -294,7 +312,7 @@ __global__ __launch_bounds__(kRouteThreads, NI > 10 ? 3 : 4) void route_fast_ker
                                                                    float* __restrict__ topk_w) {
   extern __shared__ __align__(16) char s_dyn[];
   using P = Packed<LPT, NI>;
-  constexpr int kTokens = 64 / LPT, kAll = LPT * NI * 4, MM = (KL - 1 + LPT - 1) / LPT;
+  constexpr int kTokens = 64 / LPT, kAll = LPT * NI * 4, MM = (KL - 2 + LPT - 1) / LPT;  // KL: k + 2 or more
   constexpr float kHigh = P::kTop - 64.f, kPerLogit = kHigh / kLogitRange;
   const int wv = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
   const int32_t per = a.E / a.groups, pitch = key_pitch(a.E);
@@ -549,17 +567,21 @@ __global__ __launch_bounds__(kRouteThreads, NI > 10 ? 3 : 4) void route_fast_ker
       for (int j = 0; j < KL; ++j) other[j] = dpp<decltype(ctrl)::value>(list[j]);
       insert_all<0>(list, other);
     });
-    // Is every order that counts certain?  One that is not, of two chosen, is settled by
-    // their keys in fp64; anything else is for route_token.
+    // Is every order that counts certain?  One that is not is settled by the two keys in
+    // fp64; more, or one whose lower is close to a third, are for route_token.
     uint32_t last = 0, close = 0, upper = 0, lower = 0;
     int place = 0;
+    bool before = false;
 #pragma unroll
     for (int j = 0; j < KL - 1; ++j) {
-      if (j >= a.k) continue;
+      if (j > a.k) continue;
       const uint32_t x = list[j] >> P::kIdBits, y = list[j + 1] >> P::kIdBits;
+      const bool near = y != 0 && x - y < margin;
+      again |= near && before;
+      before = near;
+      if (j == a.k) continue;
       last = x;
-      if (y != 0 && x - y < margin) {
-        if (j + 1 >= a.k) again = true;
+      if (near) {
         close += 1;
         place = j;
         upper = list[j];
@@ -569,23 +591,16 @@ __global__ __launch_bounds__(kRouteThreads, NI > 10 ? 3 : 4) void route_fast_ker
     again |= close > 1;
     const bool settle = close == 1 && !again && t < a.tokens;
     if (ballot(settle) != 0) {
-      if (with_bias && !a.sigmoid) {
-        again |= settle;  // their scores hang on all of the row
-      } else {
-        const int32_t e0 = static_cast<int32_t>(P::kIds - (upper & P::kIds)), e1 = static_cast<int32_t>(P::kIds - (lower & P::kIds));
-        double k0 = 0.0, k1 = 0.0;
-        if (settle) {
-          const float l0 = load_logit(a, t * E + e0), l1 = load_logit(a, t * E + e1);
-          k0 = with_bias ? score_of(true, l0, Soft{}) + static_cast<double>(a.bias[e0]) : static_cast<double>(l0);
-          k1 = with_bias ? score_of(true, l1, Soft{}) + static_cast<double>(a.bias[e1]) : static_cast<double>(l1);
-        }
-        const bool swap = settle && (k1 > k0 || (k1 == k0 && e1 < e0));
+      const int32_t e0 = static_cast<int32_t>(P::kIds - (upper & P::kIds)), e1 = static_cast<int32_t>(P::kIds - (lower & P::kIds));
+      bool sure = true;
+      const double d = settle ? exact_difference(a, t * E, e0, e1, top, inv, sure) : 0.0;
+      again |= settle && !sure;
+      const bool swap = settle && (d < 0.0 || (d == 0.0 && e1 < e0));
 #pragma unroll
-        for (int j = 0; j < KL - 2; ++j) {
-          if (swap && j == place) {
-            list[j] = lower;
-            list[j + 1] = upper;
-          }
+      for (int j = 0; j < KL - 1; ++j) {
+        if (swap && j == place) {
+          list[j] = lower;
+          list[j + 1] = upper;
         }
       }
     }
@@ -606,7 +621,7 @@ __global__ __launch_bounds__(kRouteThreads, NI > 10 ? 3 : 4) void route_fast_ker
       uint32_t k_j = 0;
 #pragma unroll
       for (int c = 0; c < LPT; ++c)
-        if (mm * LPT + c < KL - 1) k_j = q == c ? list[mm * LPT + c < KL ? mm * LPT + c : 0] : k_j;
+        if (mm * LPT + c < KL - 2) k_j = q == c ? list[mm * LPT + c < KL ? mm * LPT + c : 0] : k_j;
       const bool some = (k_j >> P::kIdBits) != 0 && mm * LPT + q < a.k && t < a.tokens;
       e_j[mm] = some ? static_cast<int32_t>(P::kIds - (k_j & P::kIds)) : -1;
       l_j[mm] = some ? load_logit(a, t * E + e_j[mm]) : 0.f;
@@ -852,7 +867,7 @@ void launch_fast(const RouteArgs& a, int32_t* idx, float* w, hipStream_t st) {
 
 template <int LPT, int NI>
 void launch_fast_of(const RouteArgs& a, int32_t* idx, float* w, hipStream_t st) {
-  (a.k <= 4 ? launch_fast<LPT, NI, 5> : a.k <= 8 ? launch_fast<LPT, NI, 9> : launch_fast<LPT, NI, 13>)(a, idx, w, st);
+  (a.k <= 4 ? launch_fast<LPT, NI, 6> : a.k <= 8 ? launch_fast<LPT, NI, 10> : launch_fast<LPT, NI, 14>)(a, idx, w, st);
 }
 
 // Whether the kernel for many tokens a wave takes the call.
