@@ -307,8 +307,12 @@ __host__ __device__ inline int32_t wave_words(const RouteArgs& a) {
   return a.groups > 1 ? 64 / LPT * (key_pitch(a.E) + kFastGroups) : 2 * a.E;
 }
 
+// Workgroups that fit a CU by the registers they are given.
+template <int LPT, int NI>
+constexpr int kRouteFit = NI > 10 ? 3 : 4;
+
 template <int LPT, int NI, int KL>
-__global__ __launch_bounds__(kRouteThreads, NI > 10 ? 3 : 4) void route_fast_kernel(RouteArgs a, int32_t* __restrict__ topk_idx,
+__global__ __launch_bounds__(kRouteThreads, (kRouteFit<LPT, NI>)) void route_fast_kernel(RouteArgs a, int32_t* __restrict__ topk_idx,
                                                                    float* __restrict__ topk_w) {
   extern __shared__ __align__(16) char s_dyn[];
   using P = Packed<LPT, NI>;
@@ -544,8 +548,60 @@ __global__ __launch_bounds__(kRouteThreads, NI > 10 ? 3 : 4) void route_fast_ker
           out = fmaxf(out, 0.f);
         }
       }
-      const float gap = token_min<LPT>(in) - token_max<LPT>(out);  // infinite where there is no other
-      again |= gap < apart;
+      in = token_min<LPT>(in);
+      out = token_max<LPT>(out);
+      const bool unsure = in - out < apart && t < a.tokens;  // the last that stays and the first that goes
+      if (ballot(unsure) != 0) {
+        // These two in fp64, one by the token's first lane and one by its second, where no
+        // third is close to them nor to the two experts that their keys are made of.
+        float better = __builtin_huge_valf(), worse = -__builtin_huge_valf();
+        uint32_t ids[2] = {0, 0};
+#pragma unroll
+        for (int gi = 0; gi < kOwn; ++gi) {
+          if (worth[gi] < 0.f) continue;
+          const int r = rank[gi] - a.topk_groups, g = gi * LPT + q;
+          if (r == -2) better = worth[gi];
+          if (r == 1) worse = worth[gi];
+          if (r == -1) ids[0] = g + 1;
+          if (r == 0) ids[1] = g + 1;
+        }
+        const int32_t g0 = static_cast<int32_t>(token_or<LPT>(ids[0])) - 1, g1 = static_cast<int32_t>(token_or<LPT>(ids[1])) - 1;
+        bool sure = token_min<LPT>(better) - out >= apart && in - token_max<LPT>(worse) >= apart && g0 >= 0 && g1 >= 0 &&
+                    (with_bias || a.bf16 || in >= apart);
+        double s = 0.0, b = 0.0;
+        if (unsure && sure && q < 2) {
+          uint32_t k[3] = {0, 0, 0};
+          const uint32_t* group = row + (q == 0 ? g0 : g1) * per;
+          for (int j = 0; j < per; ++j) insert<0>(k, group[j]);
+          const int n = a.group_top;
+          const uint32_t x = (n == 1 ? k[0] : k[1]) >> P::kIdBits, y = (n == 1 ? k[1] : k[2]) >> P::kIdBits;
+          sure = y == 0 || x - y >= margin;
+#pragma unroll 1
+          for (int i = 0; i < n; ++i) {
+            const uint32_t key = i == 0 ? k[0] : k[1];
+            if ((key >> P::kIdBits) == 0) continue;
+            const int32_t e = static_cast<int32_t>(P::kIds - (key & P::kIds));
+            const float l = load_logit(a, t * E + e);
+            const double score = n == 1 && !with_bias ? static_cast<double>(l) : score_of(a.sigmoid, l, Soft{static_cast<double>(top), 1.0});
+            const double add = with_bias ? static_cast<double>(a.bias[e]) : 0.0;
+            s += a.sigmoid ? score + add : score;
+            b += add;
+          }
+        }
+        const int first = lane - q;
+        const double s0 = __shfl(s, first), s1 = __shfl(s, first + 1), b0 = __shfl(b, first), b1 = __shfl(b, first + 1);
+        sure = __shfl(static_cast<int>(sure), first) != 0 && __shfl(static_cast<int>(sure), first + 1) != 0;
+        double d = s0 - s1;  // of a softmax without its common factor
+        if (!a.sigmoid && with_bias) {
+          const double scores = d * inv;
+          d = scores + (b0 - b1);
+          sure = sure && fabs(d) > fabs(scores) * 0x1p-19 + 0x1p-40;
+        } else if (!a.sigmoid && a.group_top == 2) {
+          sure = sure && (d == 0.0 || fabs(d) > 0x1p-40);
+        }
+        if (unsure && sure && (d < 0.0 || (d == 0.0 && g1 < g0))) taken ^= (1u << g0) | (1u << g1);
+        again |= unsure && !sure;
+      }
       for (int s = 0; s < a.topk_groups; ++s) {
         const bool some = taken != 0;
         const int g = some ? __builtin_ctz(taken) : 0;
@@ -859,7 +915,7 @@ void launch_fast(const RouteArgs& a, int32_t* idx, float* w, hipStream_t st) {
   constexpr int kTokens = 64 / LPT;
   const size_t lds = 4 * (LPT * NI * 4 + kRouteWaves * wave_words<LPT>(a));
   // as many workgroups as fit the CUs at once, by registers (three or four) and by LDS
-  const int64_t fit = NI > 10 ? 3 : 4, by_lds = (160 << 10) / static_cast<int64_t>(lds);
+  const int64_t fit = kRouteFit<LPT, NI>, by_lds = (160 << 10) / static_cast<int64_t>(lds);
   const int64_t want = (a.tokens + kTokens * kRouteWaves - 1) / (kTokens * kRouteWaves), most = 256 * (fit < by_lds ? fit : by_lds);
   hipLaunchKernelGGL((route_fast_kernel<LPT, NI, KL>), dim3(static_cast<uint32_t>(want < most ? want : most)), dim3(kRouteThreads),
                      lds, st, a, idx, w);
