@@ -25,8 +25,9 @@
  * combine_backward's weight gradients; residual_norm_backward takes the sum of what
  * comes back to the norm's rows.
  *
- * Every result is the same for the same call, and a token's or row's results do
- * not depend on the others' (but for grad_weight, a sum over the rows).
+ * Every result is the same for the same call.  A token's or row's results do not
+ * depend on the others' (but for grad_weight, a sum over the rows); the last bits of
+ * routing weights go by E, k, groups and the number of tokens, which choose the kernel.
  */
 #ifndef ULTRAEP_LAYER_H
 #define ULTRAEP_LAYER_H
