@@ -173,9 +173,10 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a, int32
 // Errors in units of 2^-24 (of the keys' range, which is at least 1): v_exp_f32 and
 // v_rcp_f32 are off by a step, so a sigmoid by 3.9, a softmax by 27 with its sum; bias,
 // fma and the cut to whole numbers add 2.5.  Bound by instructions: 262144 tokens of 256
-// experts in 8 groups, 285 MB, 106 us (55 at the rate of a large copy; 100 without any
-// token done again, 90 without reading the chosen logits a second time); 524288 of 128
-// without groups, 302 MB, 83 us.  One wave a token, all in fp64: 616 and 821.
+// experts in 8 groups, 285 MB, 102 us (55 at the rate of a large copy; 95 without any
+// token done again); 524288 of 128 without groups, 302 MB, 75 us.  One wave a token, all in
+// fp64: 616 and 821.  Logits read a round ahead: 106 and 83, as the chosen ones, read
+// again for their weights, have left the L2 by then.
 template <int LPT, int NI>
 struct Packed {
   static constexpr int kIdBits = LPT * NI * 4 <= 256 ? 8 : 9;
@@ -374,7 +375,6 @@ __global__ __launch_bounds__(kRouteThreads, (kRouteFit<LPT, NI>)) void route_fas
     }
   };
   int64_t batch = static_cast<int64_t>(blockIdx.x) * kRouteWaves + wv;
-  load(batch, lane_id(), a.E);
   for (; batch * kTokens < a.tokens; batch += step) {
     // Made anew in every round: what hangs on them is cheap, and kept in registers (a
     // few for every expert of the lane) would push the logits out.
@@ -383,6 +383,8 @@ __global__ __launch_bounds__(kRouteThreads, (kRouteFit<LPT, NI>)) void route_fas
     asm volatile("" : "+v"(lane), "+s"(E));
     const int q = lane % LPT, tl = lane / LPT;
     const int64_t t = batch * kTokens + tl;
+    // (Not a round ahead: the chosen ones are read again, and should be in the L2 still.)
+    load(batch, lane, E);
 #pragma unroll
     for (int i = 0; i < NI; ++i)
       if ((i + 1) * LPT * 4 > E) {
@@ -478,7 +480,6 @@ __global__ __launch_bounds__(kRouteThreads, (kRouteFit<LPT, NI>)) void route_fas
         for (int c = 0; c < 4; ++c) x[c] = logit_value(l[4 * i + c]);
       });
     }
-    load(batch + step, lane, E);  // the next round's, on their way while this one's are chosen
     if (a.groups > 1) {
       wave_sync();
       constexpr int kOwn = (kFastGroups + LPT - 1) / LPT;
@@ -957,9 +958,9 @@ hipError_t launch_route(const RouteArgs& args, int32_t* idx, float* w, hipStream
     // Few tokens: more lanes for each, whose work is done sooner (1024 of 256 experts in
     // groups: 16 lanes 8.5 us, 8 9.3, 4 12.5; 8192: 16.8, 16.3, 19.6).  Many: fewer, which
     // merge less; but with groups of many experts their keys fill LDS, and smaller rounds let
-    // more waves in (262144 tokens of 256 experts: 8 lanes 104 us, 4 108; of 128 in groups
-    // 65536: 26 and 24; 524288 of 128 without groups: 98 and 84).
-    const int lanes = a.E > 256 ? 8 : a.tokens <= 4096 ? 16 : a.tokens <= 16384 || (a.groups > 1 && a.E > 128) ? 8 : 4;
+    // more waves in (262144 tokens of 256 experts: 8 lanes 102 us, 4 105; 65536 of 160 in
+    // groups: 29 and 26; 524288 of 128 without groups: 98 and 75).
+    const int lanes = a.E > 256 ? 8 : a.tokens <= 4096 ? 16 : a.tokens <= 16384 || (a.groups > 1 && a.E > 160) ? 8 : 4;
     const auto go = lanes == 16  ? (a.E <= 128 ? launch_fast_of<16, 2> : launch_fast_of<16, 4>)
                     : lanes == 8 ? (a.E <= 128   ? launch_fast_of<8, 4>
                                     : a.E <= 256 ? launch_fast_of<8, 8>

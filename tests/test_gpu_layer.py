@@ -139,6 +139,17 @@ def test_route_of_an_infinite_bias():
     check_route(v, l, 4, b, score=0)
 
 
+@pytest.mark.parametrize("E,taken", [(16, 5), (64, 9)])
+def test_route_groups_of_one_expert(E, taken):
+    rng = np.random.default_rng(E)
+    for bf16 in (False, True):
+        l, v = logits_of(rng.standard_normal((90, E)), bf16)
+        for bias in (None, rng.standard_normal(E) * 0.1):
+            for top in (1, 2):
+                idx = check_route(v, l, 8, bias, score=1, groups=E, topk_groups=taken, group_top=top)
+                assert (idx >= 0).sum() == 90 * min(taken, 8)
+
+
 @pytest.mark.parametrize("scale", [0.0, -1.5])
 def test_route_scales(scale):
     rng = np.random.default_rng(8)
