@@ -1,6 +1,6 @@
 """Build the HIP library in place: ``libultraep.so`` next to this file.
 
-One hipcc invocation compiles every source under ``csrc/`` for gfx950.
+hipcc compiles every source under ``csrc/`` for gfx950.
 Packed-fp32 instruction selection is switched off for all device code.
 """
 from __future__ import annotations
@@ -8,6 +8,8 @@ from __future__ import annotations
 import os
 import shutil
 import subprocess
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -33,15 +35,26 @@ def command(out: str = LIB) -> list:
             *[os.path.join(CSRC, s) for s in SOURCES], "-o", out]
 
 
-def build(verbose: bool = False) -> str:
-    """Compile the library (always recompiles) and return its path."""
-    tmp = LIB + ".tmp"
-    cmd = command(tmp)
-    if verbose:
-        print(" ".join(cmd), flush=True)
+def _run(cmd: list) -> None:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"hipcc failed ({r.returncode}):\n{r.stdout}\n{r.stderr}")
+
+
+def build(verbose: bool = False) -> str:
+    """Compile the library (always recompiles) and return its path.
+
+    What command() does, each source by a compiler of its own, as many at once as there are CPUs (at most 8)."""
+    tmp = LIB + ".tmp"
+    if verbose:
+        print(" ".join(command(tmp)), flush=True)
+    flags = [a for a in command(tmp)[:-2] if a != "-shared" and not a.endswith(".hip")]
+    with tempfile.TemporaryDirectory() as folder, ThreadPoolExecutor(min(8, os.cpu_count() or 1)) as pool:
+        objects = [os.path.join(folder, s + ".o") for s in SOURCES]
+        jobs = [pool.submit(_run, [*flags, "-c", os.path.join(CSRC, s), "-o", o]) for s, o in zip(SOURCES, objects)]
+        for j in jobs:
+            j.result()
+        _run([hipcc(), "--offload-arch=gfx950", "-fPIC", "-shared", *objects, "-o", tmp])
     os.replace(tmp, LIB)
     return LIB
 
