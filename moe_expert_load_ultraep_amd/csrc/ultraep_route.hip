@@ -520,7 +520,7 @@ __global__ __launch_bounds__(kRouteThreads, (kRouteFit<LPT, NI>)) void route_fas
                 float x;
                 if (a.bf16) {
                   uint32_t u = (v - 1) << 16;
-                  u ^= static_cast<uint32_t>(~(static_cast<int32_t>(u) >> 31)) | 0x80000000u;
+                  u ^= (static_cast<uint32_t>(~(static_cast<int32_t>(u) >> 31)) | 0x80000000u) & 0xFFFF0000u;
                   x = __builtin_bit_cast(float, u);
                 } else {
                   x = top + (static_cast<float>(v) - kHigh) * (1.f / kPerLogit);

@@ -1,0 +1,53 @@
+"""Choices of the routing that hang on how its keys and its groups' keys are made, ids against the 64-bit oracle.
+
+Every row is checked in batches of three lengths, which reach the kernel's three ways of dealing lanes to tokens."""
+import numpy as np
+import pytest
+
+import moe_expert_load_ultraep_amd as U
+import oracle.layer_oracle as Y
+from test_gpu_layer import ctx_of, dev, host, logits_of, weight_slack
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+DEV = "cuda"
+BATCHES = (24, 6000, 40000)
+INF, NAN = np.inf, np.nan
+
+
+def check(x, k, bf16=False, bias=None, batches=BATCHES, **kw):
+    """The rows x again and again to the batch's length; the oracle's ids of each."""
+    l, v = logits_of(x, bf16)
+    b = None if bias is None else np.asarray(bias, dtype=np.float32)
+    idx_kw = dict(groups=kw.get("groups", 1), topk_groups=kw.get("topk_groups", 1), group_top=kw.get("group_top", 1))
+    score, renorm = kw.get("score", 0), kw.get("renormalize", True)
+    want, want_w = Y.route(v, k, bool(score), b, renorm=renorm, **idx_kw)
+    slack = weight_slack(v, want, score, renorm)[:, None] * want_w + 2.0 ** -120
+    for tokens in batches:
+        times = -(-tokens // len(v))
+        many = l.repeat(times, 1)[:tokens].contiguous()
+        idx = torch.full((tokens, k), -77, dtype=torch.int32, device=DEV)
+        w = torch.full((tokens, k), -7.0, device=DEV)
+        U.ultraep_route(ctx_of(l.shape[1]), many, k, idx, w, bias=None if b is None else dev(b), **kw)
+        got, rows = host(idx), np.arange(tokens) % len(v)
+        wrong = (got != want[rows]).any(axis=1)
+        assert not wrong.any(), (tokens, int(wrong.sum()), v[rows[wrong][0]].tolist(), got[wrong][0].tolist(), want[rows[wrong][0]].tolist())
+        assert (np.abs(host(w) - want_w[rows]) <= slack[rows]).all()
+    return want
+
+
+# ---------------------------------------------------------------- bf16 logits, sums of two scores
+
+def test_two_scores_of_negative_bf16_logits_by_hand():
+    """sigmoid(0.5) + sigmoid(-20) = 0.62246 against sigmoid(0) + sigmoid(-1.96875) = 0.62253."""
+    x = np.array([[0.5, -20.0, 0.0, -1.96875]])
+    assert check(x, 1, bf16=True, score=1, groups=2, topk_groups=1, group_top=2).tolist() == [[2]]
+
+
+@pytest.mark.parametrize("E,groups,taken", [(16, 8, 2), (60, 10, 8), (128, 8, 4), (160, 8, 3), (256, 8, 4), (512, 16, 5)])
+@pytest.mark.parametrize("score", [0, 1])
+@pytest.mark.parametrize("mean", [-3.0, 0.0])
+def test_two_scores_of_bf16_logits(E, groups, taken, score, mean):
+    rng = np.random.default_rng(E)
+    check(rng.standard_normal((400, E)) + mean, min(8, E), bf16=True, score=score, groups=groups, topk_groups=taken, group_top=2)
