@@ -257,6 +257,7 @@ __host__ __device__ inline int32_t key_pitch(int32_t E) { return E + ((16 - E) &
 
 struct KeyUnits {
   float c;        // units of a score
+  float one;      // units that a sum of two keys is above a single key of the same worth
   bool exact;     // the bias spans too much for them
 };
 
@@ -289,7 +290,8 @@ __device__ __forceinline__ KeyUnits bias_units(const RouteArgs& a, float* table)
     hi = fmaxf(hi, s_hi[i]);
   }
   const float span = hi - lo + 1.f;
-  KeyUnits u{(Packed<LPT, NI>::kTop - 64.f) / span, !(span < 1e4f)};
+  KeyUnits u{(Packed<LPT, NI>::kTop - 64.f) / span, 0.f, !(span < 1e4f)};
+  u.one = 8.f - lo * u.c;
   for (int e = tid; e < kAll; e += kRouteThreads) {
     const float b = e < a.E ? a.bias[e] : __builtin_nanf("");
     table[e] = b > -__builtin_huge_valf() ? (b - lo) * u.c + 8.f : __builtin_nanf("");
@@ -340,7 +342,7 @@ __global__ __launch_bounds__(kRouteThreads, (kRouteFit<LPT, NI>)) void route_fas
   float* worths = reinterpret_cast<float*>(keys + kTokens * pitch);
   const bool with_bias = a.bias != nullptr;
   const bool in_fours = a.E % 4 == 0 && reinterpret_cast<uintptr_t>(a.logits) % 8 == 0;  // bf16
-  KeyUnits units{0.f, false};
+  KeyUnits units{0.f, 0.f, false};
   if (with_bias) units = bias_units<LPT, NI>(a, bias);
   // what two keys have to be apart for their order to be certain, in units
   const uint32_t margin = with_bias ? (a.sigmoid ? (P::kIdBits == 8 ? 13u : 9u) : (P::kIdBits == 8 ? 64u : 40u)) : a.bf16 ? 0u : 8u;
@@ -483,12 +485,14 @@ __global__ __launch_bounds__(kRouteThreads, (kRouteFit<LPT, NI>)) void route_fas
     if (a.groups > 1) {
       wave_sync();
       constexpr int kOwn = (kFastGroups + LPT - 1) / LPT;
+      constexpr float kNoWorth = -__builtin_huge_valf();  // of a group without an expert to choose
       float worth[kOwn];
+      uint32_t alone = 0;  // is there a group with one expert to choose, where others may have two?
       const uint32_t* row = keys + tl * pitch;
 #pragma unroll
       for (int gi = 0; gi < kOwn; ++gi) {
         const int g = gi * LPT + q;
-        worth[gi] = -1.f;
+        worth[gi] = kNoWorth;
         if (gi * LPT < a.groups) {
           uint32_t first = 0, second = 0;
           if (g < a.groups) {
@@ -512,6 +516,10 @@ __global__ __launch_bounds__(kRouteThreads, (kRouteFit<LPT, NI>)) void route_fas
               worth[gi] = static_cast<float>(first);
             } else if (with_bias) {
               worth[gi] = static_cast<float>(first + second);
+              if (second == 0 && per > 1) {
+                worth[gi] += units.one;
+                alone = 1;
+              }
             } else {  // scores of the two logits, up to the softmax's common factor
               float s = 0.f;
 #pragma unroll
@@ -548,14 +556,17 @@ __global__ __launch_bounds__(kRouteThreads, (kRouteFit<LPT, NI>)) void route_fas
       float in = __builtin_huge_valf(), out = -__builtin_huge_valf();
 #pragma unroll
       for (int gi = 0; gi < kOwn; ++gi) {
-        const bool mine = worth[gi] >= 0.f, take = mine && rank[gi] < a.topk_groups;
+        const bool mine = worth[gi] > kNoWorth, take = mine && rank[gi] < a.topk_groups;
         if (take) taken |= 1u << (gi * LPT + q);
         if (take) in = fminf(in, worth[gi]);
         if (mine && !take) out = fmaxf(out, worth[gi]);
       }
       taken = token_or<LPT>(taken);
       float apart = static_cast<float>(margin);
-      if (a.group_top == 2 && with_bias) apart = 2.f * apart + 4.f;
+      if (a.group_top == 2 && with_bias) {
+        apart = 2.f * apart + 4.f;
+        if (token_or<LPT>(alone) != 0) apart += fabsf(units.one) * 0x1p-22f;  // it is rounded twice, its sum once
+      }
       if (a.group_top == 2 && !with_bias) {
         apart = 1e-5f;
         if (!a.bf16) {  // logits below the keys' range have scores up to this
@@ -573,7 +584,7 @@ __global__ __launch_bounds__(kRouteThreads, (kRouteFit<LPT, NI>)) void route_fas
         uint32_t ids[2] = {0, 0};
 #pragma unroll
         for (int gi = 0; gi < kOwn; ++gi) {
-          if (worth[gi] < 0.f) continue;
+          if (worth[gi] == kNoWorth) continue;
           const int r = rank[gi] - a.topk_groups, g = gi * LPT + q;
           if (r == -2) better = worth[gi];
           if (r == 1) worse = worth[gi];

@@ -51,3 +51,41 @@ def test_two_scores_of_negative_bf16_logits_by_hand():
 def test_two_scores_of_bf16_logits(E, groups, taken, score, mean):
     rng = np.random.default_rng(E)
     check(rng.standard_normal((400, E)) + mean, min(8, E), bf16=True, score=score, groups=groups, topk_groups=taken, group_top=2)
+
+
+# ---------------------------------------------------------------- groups with one expert left beside groups with more
+
+def alone(rng, E, groups, rows=400):
+    """Rows in which some groups keep one expert, some two and some all, the others none."""
+    per = E // groups
+    x = rng.standard_normal((rows, E)) * 1.3
+    keep = rng.choice([0, 1, 1, 2, per], size=(rows, groups))
+    place = np.argsort(rng.random((rows, groups, per)), axis=2)
+    gone = (place >= keep[:, :, None]).reshape(rows, E)
+    return np.where(gone, rng.choice([-INF, NAN], size=(rows, E)), x)
+
+
+def test_a_group_with_one_expert_left_by_hand():
+    """0.9003 alone against 0.4013 twice: less the smallest bias, -0.3, once and twice."""
+    x = np.array([[2.2, -INF, -INF, -INF] + [-0.4] * 4 + [-0.6] * 4 + [-5.0] * 4])
+    bias = np.zeros(16)
+    bias[12] = -0.3
+    assert check(x, 2, bias=bias, score=1, groups=4, topk_groups=1, group_top=2).tolist() == [[0, -1]]
+
+
+@pytest.mark.parametrize("E,groups,taken", [(16, 4, 1), (16, 8, 3), (60, 10, 4), (64, 16, 5), (128, 8, 4), (160, 8, 3), (256, 8, 4), (512, 16, 5)])
+@pytest.mark.parametrize("score", [0, 1])
+@pytest.mark.parametrize("shift", [0.0, 1.0, -1.0, 40.0, -300.0])
+def test_groups_with_one_expert_left(E, groups, taken, score, shift):
+    rng = np.random.default_rng(E + groups)
+    bias = shift + rng.standard_normal(E) * 0.1
+    how = dict(score=score, groups=groups, topk_groups=taken, group_top=2)
+    for bf16 in (False, True):
+        check(alone(rng, E, groups), 4, bf16=bf16, bias=bias, **how)
+    # by the bias: the first group keeps one expert, the second none, the third two
+    per = E // groups
+    if per > 2:
+        bias[1:per], bias[per:2 * per], bias[2 * per + 2:3 * per] = -INF, NAN, -INF
+    else:
+        bias[1], bias[2:4] = -INF, NAN
+    check(rng.standard_normal((400, E)) * 1.3, 4, bias=bias, **how)
