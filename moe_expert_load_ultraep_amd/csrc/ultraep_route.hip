@@ -601,7 +601,8 @@ __global__ __launch_bounds__(kRouteThreads, (kRouteFit<LPT, NI>)) void route_fas
           for (int j = 0; j < per; ++j) insert<0>(k, group[j]);
           const int n = a.group_top;
           const uint32_t x = (n == 1 ? k[0] : k[1]) >> P::kIdBits, y = (n == 1 ? k[1] : k[2]) >> P::kIdBits;
-          sure = y == 0 || x - y >= margin;
+          // (A key of 0 is no expert; of fp32 logits without a bias it may be one below the keys' range.)
+          sure = per == 1 || (y == 0 && (with_bias || a.bf16)) || x - y >= margin;
 #pragma unroll 1
           for (int i = 0; i < n; ++i) {
             const uint32_t key = i == 0 ? k[0] : k[1];

@@ -89,3 +89,34 @@ def test_groups_with_one_expert_left(E, groups, taken, score, shift):
     else:
         bias[1], bias[2:4] = -INF, NAN
     check(rng.standard_normal((400, E)) * 1.3, 4, bias=bias, **how)
+
+
+# ---------------------------------------------------------------- fp32 logits more than 16 below the row's largest
+
+def test_a_second_score_far_below_the_largest_logit_by_hand():
+    """Sums of two scores: 0.99995 and 0.99995 + 0.0015; 1 and 2^-7.2 each but for a far smaller term."""
+    x = np.array([[10.0, -100.0, 9.9, -6.5]])
+    assert check(x, 1, score=1, groups=2, topk_groups=1, group_top=2).tolist() == [[2]]
+    x = np.array([[10.0, 0.0, 5.0, -100.0, 5.0, -6.5, 0.0, 0.0]])
+    assert check(x, 2, score=0, groups=4, topk_groups=2, group_top=2).tolist() == [[0, 4]]
+
+
+@pytest.mark.parametrize("E,groups,taken", [(8, 4, 2), (16, 4, 1), (64, 16, 5), (96, 6, 2), (128, 8, 4), (160, 8, 3), (256, 8, 4), (512, 16, 5)])
+@pytest.mark.parametrize("score", [0, 1])
+@pytest.mark.parametrize("top", [1, 2])
+@pytest.mark.parametrize("spread,mean", [(20.0, 0.0), (20.0, -30.0), (60.0, 10.0), (6.0, 0.0)])
+def test_logits_of_a_wide_spread(E, groups, taken, score, top, spread, mean):
+    """Some groups have the same best, and seconds that lie far below or are masked."""
+    rng = np.random.default_rng(E + groups)
+    x = rng.standard_normal((300, E)) * spread + mean
+    per = E // groups
+    for t in range(0, 300, 2):
+        a, b = rng.choice(groups, 2, replace=False)
+        best = x[t].max() - rng.choice([0.0, 3.0, 8.0, 15.0, 20.0])
+        x[t, a * per:(a + 1) * per] = best - 16 - rng.random(per) * 20
+        x[t, b * per:(b + 1) * per] = best - 16 - rng.random(per) * 20
+        x[t, a * per] = best
+        x[t, b * per + per - 1] = best - rng.choice([0.0, 1e-6, 1e-4])
+        if t % 8 == 0:
+            x[t, b * per:(b + 1) * per - 1] = rng.choice([-INF, NAN])
+    check(x, min(4, E), score=score, groups=groups, topk_groups=taken, group_top=top)
