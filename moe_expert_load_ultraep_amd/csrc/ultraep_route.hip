@@ -258,7 +258,8 @@ __host__ __device__ inline int32_t key_pitch(int32_t E) { return E + ((16 - E) &
 struct KeyUnits {
   float c;        // units of a score
   float one;      // units that a sum of two keys is above a single key of the same worth
-  bool exact;     // the bias spans too much for them
+  float fine;     // keys in fp64 nearer than this may be in another order by their own rounding
+  bool exact;     // the bias spans too much for them, or is too large
 };
 
 // The bias in units of the keys, in LDS; absent experts' are NaN, which gives no key.
@@ -290,7 +291,10 @@ __device__ __forceinline__ KeyUnits bias_units(const RouteArgs& a, float* table)
     hi = fmaxf(hi, s_hi[i]);
   }
   const float span = hi - lo + 1.f;
-  KeyUnits u{(Packed<LPT, NI>::kTop - 64.f) / span, 0.f, !(span < 1e4f)};
+  // Sums with a bias are rounded to 2^-53 of it, which below 2^20 is far less than a unit;
+  // two sums of two of them, to 2^-50.
+  const float size = fmaxf(-lo, hi);
+  KeyUnits u{(Packed<LPT, NI>::kTop - 64.f) / span, 0.f, 0x1p-40f + size * 0x1p-49f, !(span < 1e4f && size < 0x1p20f)};
   u.one = 8.f - lo * u.c;
   for (int e = tid; e < kAll; e += kRouteThreads) {
     const float b = e < a.E ? a.bias[e] : __builtin_nanf("");
@@ -304,7 +308,7 @@ __device__ __forceinline__ KeyUnits bias_units(const RouteArgs& a, float* table)
 // is taken by its sum in fp32 (inv, its inverse), off by less than 2^-19: where that could
 // decide, the answer is not sure.
 __device__ __forceinline__ double exact_difference(const RouteArgs& a, int64_t row, int32_t e0, int32_t e1, float top, float inv,
-                                                   bool& sure) {
+                                                   float fine, bool& sure) {
   const double l0 = static_cast<double>(load_logit(a, row + e0)), l1 = static_cast<double>(load_logit(a, row + e1));
   if (a.bias == nullptr) return l0 - l1;
   const double b = static_cast<double>(a.bias[e0]) - static_cast<double>(a.bias[e1]);
@@ -314,7 +318,7 @@ __device__ __forceinline__ double exact_difference(const RouteArgs& a, int64_t r
     return k0 - k1;
   }
   const double s = (exp(l0 - top) - exp(l1 - top)) * inv, d = s + b;
-  sure = fabs(d) > fabs(s) * 0x1p-19 + 0x1p-40;
+  sure = fabs(d) > fabs(s) * 0x1p-19 + fine;
   return d;
 }
 
@@ -342,7 +346,7 @@ __global__ __launch_bounds__(kRouteThreads, (kRouteFit<LPT, NI>)) void route_fas
   float* worths = reinterpret_cast<float*>(keys + kTokens * pitch);
   const bool with_bias = a.bias != nullptr;
   const bool in_fours = a.E % 4 == 0 && reinterpret_cast<uintptr_t>(a.logits) % 8 == 0;  // bf16
-  KeyUnits units{0.f, 0.f, false};
+  KeyUnits units{0.f, 0.f, 0.f, false};
   if (with_bias) units = bias_units<LPT, NI>(a, bias);
   // what two keys have to be apart for their order to be certain, in units
   const uint32_t margin = with_bias ? (a.sigmoid ? (P::kIdBits == 8 ? 13u : 9u) : (P::kIdBits == 8 ? 64u : 40u)) : a.bf16 ? 0u : 8u;
@@ -622,7 +626,7 @@ __global__ __launch_bounds__(kRouteThreads, (kRouteFit<LPT, NI>)) void route_fas
         if (!a.sigmoid && with_bias) {
           const double scores = d * inv;
           d = scores + (b0 - b1);
-          sure = sure && fabs(d) > fabs(scores) * 0x1p-19 + 0x1p-40;
+          sure = sure && fabs(d) > fabs(scores) * 0x1p-19 + units.fine;
         } else if (!a.sigmoid && a.group_top == 2) {
           sure = sure && (d == 0.0 || fabs(d) > 0x1p-40);
         }
@@ -676,7 +680,7 @@ __global__ __launch_bounds__(kRouteThreads, (kRouteFit<LPT, NI>)) void route_fas
     if (ballot(settle) != 0) {
       const int32_t e0 = static_cast<int32_t>(P::kIds - (upper & P::kIds)), e1 = static_cast<int32_t>(P::kIds - (lower & P::kIds));
       bool sure = true;
-      const double d = settle ? exact_difference(a, t * E, e0, e1, top, inv, sure) : 0.0;
+      const double d = settle ? exact_difference(a, t * E, e0, e1, top, inv, units.fine, sure) : 0.0;
       again |= settle && !sure;
       const bool swap = settle && (d < 0.0 || (d == 0.0 && e1 < e0));
 #pragma unroll

@@ -120,3 +120,19 @@ def test_logits_of_a_wide_spread(E, groups, taken, score, top, spread, mean):
         if t % 8 == 0:
             x[t, b * per:(b + 1) * per - 1] = rng.choice([-INF, NAN])
     check(x, min(4, E), score=score, groups=groups, topk_groups=taken, group_top=top)
+
+
+# ---------------------------------------------------------------- large biases
+
+@pytest.mark.parametrize("size", [700.0, -5e3, 6e4, 1e6, -1e7, 1e10, -3e30])
+@pytest.mark.parametrize("E,groups,taken,top", [(32, 1, 1, 1), (60, 4, 2, 2), (128, 8, 4, 1), (160, 8, 3, 2), (256, 8, 4, 2), (400, 8, 3, 2)])
+@pytest.mark.parametrize("score", [0, 1])
+def test_biases_that_are_large(E, groups, taken, top, score, size):
+    """Scores plus bias tie in 64 bits, or nearly so: the lower id, and the lower group, go first there."""
+    rng = np.random.default_rng(E)
+    x = rng.standard_normal((200, E)) * rng.choice([1.0, 12.0], size=(200, 1))
+    x[::5] = np.round(x[::5])
+    how = dict(score=score, groups=groups, topk_groups=taken, group_top=top)
+    for bias in (np.full(E, size), size + rng.integers(0, 4, E) * max(1.0, abs(size) * 2.0 ** -22), size + rng.standard_normal(E) * 50,
+                 np.where(rng.random(E) < 0.2, size, rng.standard_normal(E) * 0.05)):
+        check(x, min(8, E), bias=bias, **how)
