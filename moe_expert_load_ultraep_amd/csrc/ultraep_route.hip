@@ -628,7 +628,7 @@ __global__ __launch_bounds__(kRouteThreads, (kRouteFit<LPT, NI>)) void route_fas
           d = scores + (b0 - b1);
           sure = sure && fabs(d) > fabs(scores) * 0x1p-19 + units.fine;
         } else if (!a.sigmoid && a.group_top == 2) {
-          sure = sure && (d == 0.0 || fabs(d) > 0x1p-40);
+          sure = sure && fabs(d) > 0x1p-40;  // also where it is 0, as the common factor rounds the scores
         }
         if (unsure && sure && (d < 0.0 || (d == 0.0 && g1 < g0))) taken ^= (1u << g0) | (1u << g1);
         again |= unsure && !sure;

@@ -136,3 +136,15 @@ def test_biases_that_are_large(E, groups, taken, top, score, size):
     for bias in (np.full(E, size), size + rng.integers(0, 4, E) * max(1.0, abs(size) * 2.0 ** -22), size + rng.standard_normal(E) * 50,
                  np.where(rng.random(E) < 0.2, size, rng.standard_normal(E) * 0.05)):
         check(x, min(8, E), bias=bias, **how)
+
+
+# ---------------------------------------------------------------- sums of two scores that differ by one rounding
+
+def test_two_scores_that_differ_by_less_than_the_sum_of_exponentials_shows():
+    """Not normalised, 1 + e^-37 and 1 + e^-47 both round to 1; over the sum, 2 + e^-22.75, the first is the larger."""
+    x = np.array([[0.0, -47.0, 0.0, -37.0, -22.75, -100.0]])
+    for bf16 in (False, True):
+        assert check(x, 1, bf16=bf16, score=0, groups=3, topk_groups=1, group_top=2).tolist() == [[2]]
+    x = np.array([[0.0, -40.0, 0.0, -40.0, -22.75, -100.0]])   # the same: the lower group
+    for bf16 in (False, True):
+        assert check(x, 1, bf16=bf16, score=0, groups=3, topk_groups=1, group_top=2).tolist() == [[0]]
