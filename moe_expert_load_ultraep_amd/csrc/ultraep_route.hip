@@ -599,6 +599,7 @@ __global__ __launch_bounds__(kRouteThreads, (kRouteFit<LPT, NI>)) void route_fas
         bool sure = token_min<LPT>(better) - out >= apart && in - token_max<LPT>(worse) >= apart && g0 >= 0 && g1 >= 0 &&
                     (with_bias || a.bf16 || in >= apart);
         double s = 0.0, b = 0.0;
+        float l0 = -__builtin_huge_valf(), l1 = l0;
         if (unsure && sure && q < 2) {
           uint32_t k[3] = {0, 0, 0};
           const uint32_t* group = row + (q == 0 ? g0 : g1) * per;
@@ -613,6 +614,10 @@ __global__ __launch_bounds__(kRouteThreads, (kRouteFit<LPT, NI>)) void route_fas
             if ((key >> P::kIdBits) == 0) continue;
             const int32_t e = static_cast<int32_t>(P::kIds - (key & P::kIds));
             const float l = load_logit(a, t * E + e);
+            if (i == 0)
+              l0 = l;
+            else
+              l1 = l;
             const double score = n == 1 && !with_bias ? static_cast<double>(l) : score_of(a.sigmoid, l, Soft{static_cast<double>(top), 1.0});
             const double add = with_bias ? static_cast<double>(a.bias[e]) : 0.0;
             s += a.sigmoid ? score + add : score;
@@ -628,7 +633,9 @@ __global__ __launch_bounds__(kRouteThreads, (kRouteFit<LPT, NI>)) void route_fas
           d = scores + (b0 - b1);
           sure = sure && fabs(d) > fabs(scores) * 0x1p-19 + units.fine;
         } else if (!a.sigmoid && a.group_top == 2) {
-          sure = sure && fabs(d) > 0x1p-40;  // also where it is 0, as the common factor rounds the scores
+          // (the common factor rounds the scores, so they need not be equal where d is 0)
+          const bool same = __shfl(l0, first) == __shfl(l0, first + 1) && __shfl(l1, first) == __shfl(l1, first + 1);
+          sure = sure && (same || fabs(d) > 0x1p-40);
         }
         if (unsure && sure && (d < 0.0 || (d == 0.0 && g1 < g0))) taken ^= (1u << g0) | (1u << g1);
         again |= unsure && !sure;

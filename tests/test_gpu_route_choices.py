@@ -148,3 +148,20 @@ def test_two_scores_that_differ_by_less_than_the_sum_of_exponentials_shows():
     x = np.array([[0.0, -40.0, 0.0, -40.0, -22.75, -100.0]])   # the same: the lower group
     for bf16 in (False, True):
         assert check(x, 1, bf16=bf16, score=0, groups=3, topk_groups=1, group_top=2).tolist() == [[0]]
+
+
+@pytest.mark.parametrize("E,groups,taken", [(16, 4, 1), (128, 8, 4), (160, 8, 3), (512, 16, 5)])
+def test_two_scores_of_equal_pairs(E, groups, taken):
+    """Pairs of the same two logits, and of one alone, in several groups: the lower group; a coarse grid of values."""
+    rng = np.random.default_rng(E)
+    x = np.round(rng.standard_normal((300, E)) * 3) / 2
+    per = E // groups
+    for t in range(0, 300, 3):
+        best = x[t].max() + 1.0
+        for g in rng.choice(groups, taken + 1, replace=False):
+            x[t, g * per:g * per + 2] = rng.permutation([best, best - 0.5]) if t % 2 else [best, -INF]
+            if not t % 2:
+                x[t, g * per + 1:(g + 1) * per] = -INF
+    for bf16 in (False, True):
+        for score in (0, 1):
+            check(x, 4, bf16=bf16, score=score, groups=groups, topk_groups=taken, group_top=2)
