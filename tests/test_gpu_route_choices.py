@@ -165,3 +165,21 @@ def test_two_scores_of_equal_pairs(E, groups, taken):
     for bf16 in (False, True):
         for score in (0, 1):
             check(x, 4, bf16=bf16, score=score, groups=groups, topk_groups=taken, group_top=2)
+
+
+# ---------------------------------------------------------------- every width, list and way of dealing lanes
+
+@pytest.mark.parametrize("E,groups,taken", [(20, 5, 3), (32, 4, 2), (64, 8, 3), (128, 8, 4), (144, 9, 4), (160, 8, 3), (250, 5, 2), (256, 8, 4), (384, 12, 5),
+                                            (512, 16, 7)])
+@pytest.mark.parametrize("k", [3, 8, 12])
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("score", [0, 1])
+def test_widths_and_lists(E, groups, taken, k, bf16, score):
+    rng = np.random.default_rng(E + k)
+    for spread in (1.3, 25.0):
+        x = rng.standard_normal((70, E)) * spread
+        x[rng.random((70, E)) < 0.1] = -INF
+        for bias in (None, rng.standard_normal(E) * 0.05):
+            check(x, k, bf16=bf16, bias=bias, score=score, renormalize=spread < 2)
+            for top in (1, 2):
+                check(x, k, bf16=bf16, bias=bias, score=score, groups=groups, topk_groups=taken, group_top=top, renormalize=spread > 2)
