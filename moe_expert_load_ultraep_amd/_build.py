@@ -35,7 +35,9 @@ def command(out: str = LIB) -> list:
             *[os.path.join(CSRC, s) for s in SOURCES], "-o", out]
 
 
-def _run(cmd: list) -> None:
+def _run(cmd: list, verbose: bool) -> None:
+    if verbose:
+        print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"hipcc failed ({r.returncode}):\n{r.stdout}\n{r.stderr}")
@@ -46,15 +48,13 @@ def build(verbose: bool = False) -> str:
 
     What command() does, each source by a compiler of its own, as many at once as there are CPUs (at most 8)."""
     tmp = LIB + ".tmp"
-    if verbose:
-        print(" ".join(command(tmp)), flush=True)
     flags = [a for a in command(tmp)[:-2] if a != "-shared" and not a.endswith(".hip")]
     with tempfile.TemporaryDirectory() as folder, ThreadPoolExecutor(min(8, os.cpu_count() or 1)) as pool:
         objects = [os.path.join(folder, s + ".o") for s in SOURCES]
-        jobs = [pool.submit(_run, [*flags, "-c", os.path.join(CSRC, s), "-o", o]) for s, o in zip(SOURCES, objects)]
+        jobs = [pool.submit(_run, [*flags, "-c", os.path.join(CSRC, s), "-o", o], verbose) for s, o in zip(SOURCES, objects)]
         for j in jobs:
             j.result()
-        _run([hipcc(), "--offload-arch=gfx950", "-fPIC", "-shared", *objects, "-o", tmp])
+        _run([hipcc(), "--offload-arch=gfx950", "-fPIC", "-shared", *objects, "-o", tmp], verbose)
     os.replace(tmp, LIB)
     return LIB
 
