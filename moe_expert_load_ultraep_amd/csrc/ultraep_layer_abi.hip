@@ -125,7 +125,7 @@ int ultraep_residual_norm_backward(const ultraep_ctx* ctx, const uint16_t* grad_
   if (rows > 0 && (!grad_y || !h || !weight || !rstd || !grad_h || (grad_weight && !workspace))) return ULTRAEP_EINVAL;
   if (st != ULTRAEP_OK || !aligned(grad_y, 16) || !aligned(h, 16) || !aligned(weight, 16) || !aligned(rstd, 4) ||
       !aligned(grad_in, 16) || !aligned(grad_h, 16) || !aligned(grad_x, 16) || !aligned(grad_weight, 16) ||
-      !aligned(workspace, 16))
+      (grad_weight && !aligned(workspace, 16)))
     return ULTRAEP_EUNSUPPORTED;
   if (grad_weight && rows > 0 && workspace_bytes < ultraep::norm_workspace_bytes(rows, H)) return ULTRAEP_EWORKSPACE;
   return from_hip(ultraep::launch_norm_backward({rows, H, weight, weight_type == ULTRAEP_TYPE_BF16}, grad_y, h,
