@@ -23,7 +23,9 @@
  * ultraep_permute_quant -> ultraep_expert_gemm -> glu_quant_backward ->
  * ultraep_expert_gemm -> ultraep_combine without weights; route_backward takes
  * combine_backward's weight gradients; residual_norm_backward takes the sum of what
- * comes back to the norm's rows.
+ * comes back to the norm's rows, which the caller adds up, with the router's product.
+ * permute_quant takes the norm's bf16 rows; its 8-bit rows are for 8-bit products of all
+ * rows (a shared expert's, the attention's), which are not in this library.
  *
  * Every result is the same for the same call.  A token's or row's results do not
  * depend on the others' (but for grad_weight, a sum over the rows); the last bits of
@@ -70,7 +72,18 @@ extern "C" {
  *     and the weight 0.
  *  6. Weights: scale * s, the bias not in it; with renormalize scale * s / (the sum
  *     of the chosen experts' s), also where that sum is below fp32's range.
- * Ids are those that 64-bit arithmetic gives.
+ * Ids are those that 64-bit arithmetic gives; keys (of experts or groups) that differ by
+ * no more than its roundings may come in either order.  Weights are fp32: without
+ * renormalize scores below 2^-126 may count as zero.
+ * Nearly all tokens are settled in 32 bits.  What is not takes about ten times as long:
+ *  - tokens in whose choice two pairs of keys are equal or nearly so, or by a softmax with a
+ *    bias (also one of zeros) one pair is equal (bf16 logits without a bias excepted);
+ *  - fp32 logits without a bias, where the k-th best is more than 16 below the largest;
+ *  - group_top 2 without a bias, where three groups or more around the border are within
+ *    1e-5 of each other (all are where scores are that small, as in peaked softmaxes), or,
+ *    fp32 logits and sigmoids, within 2 / (1 + exp(16 - the largest logit));
+ *  - every token of a call whose finite biases span 1e4 or more or reach 2^20 (an expert is
+ *    switched off by -inf), or with k > 12, E > 512 or more than 16 groups.
  * In:  logits [tokens][E] of logits_type (E: the context's), bias fp32 [E] or NULL.
  * Out: topk_idx int32 [tokens][k], topk_w fp32 [tokens][k].
  * Errors: EINVAL (null pointers with tokens > 0, tokens < 0, k outside [1, min(E,
@@ -89,9 +102,10 @@ int ultraep_route(const ultraep_ctx* ctx, const void* logits, int32_t logits_typ
  *   softmax, renormalised:   dl_j = w_j * (g_j - d)
  *   softmax:                 dl_e = (w_e * g_e if chosen) - s_e * sum_i w_i * g_i
  * for the chosen experts (the last: for all that are not masked), zero for the
- * others; the choice has no gradient, nor has the bias.  Weights are computed anew
- * from the logits; an id outside [0, E) or of a masked expert has no weight and its
- * gradient is not looked at; an id that a row names twice counts twice.
+ * others, in fp32 (scores below 2^-126 may count as zero; the sums of |w * g| have to
+ * stay below its largest); the choice has no gradient, nor has the bias.  Weights are
+ * computed anew from the logits; an id outside [0, E) or of a masked expert has no weight
+ * and its gradient is not looked at; an id that a row names twice counts twice.
  * In:  logits as for ultraep_route, topk_idx int32 [tokens][k], grad_topk_w fp32
  *      [tokens][k] (from ultraep_combine_backward).
  * Out: grad_logits [tokens][E] of logits_type, every element written.
@@ -105,7 +119,8 @@ int ultraep_route_backward(const ultraep_ctx* ctx, const void* logits, int32_t l
  *   h = residual + x, rounded to the stream's type (h = x without a residual)
  *   rstd = 1 / sqrt(mean(h^2) + eps),  y = h * rstd * weight
  * in fp32; y is rounded once to bf16 for y, and from fp32 to e4m3 for the rows form.
- * The sum of a row's squares has to stay below fp32's largest (magnitudes to 2^56).
+ * The sum of a row's squares has to stay below fp32's largest (magnitudes to 2^56);
+ * with eps 0 a row whose squares are all below its range has no finite rstd.
  * In:  x [rows][H] bf16; residual [rows][H] of residual_type, or NULL; weight [H] of
  *      weight_type.
  * Out: h [rows][H] of residual_type, or NULL where the sum is not wanted or there is
@@ -155,7 +170,8 @@ int ultraep_residual_norm_backward(const ultraep_ctx* ctx, const uint16_t* grad_
  *   a[i][c] = f(h[i][c]) * h[i][F + c] for c < F, f(g) = g / (1 + exp(-z)),
  *   ULTRAEP_GLU_SILU z = g;  ULTRAEP_GLU_GELU z = 2 sqrt(2/pi) (g + 0.044715 g^3)
  * (gelu in its form by the hyperbolic tangent), in fp32, rounded once to e4m3.
- * Magnitudes below 2^-100 become zero.
+ * Magnitudes below 2^-100 become zero, and a sigmoid 1 / (1 + exp(-z)) below 2^-126 may
+ * count as zero whatever it is multiplied with.
  * In:  plan (one record); h [capacity_rows][2F] bf16, the segment's rows in order
  *      (the first product's output: gate columns, then the others).
  * Out: the rows form of a in q [capacity_rows][Fp] and q_scale [capacity_rows][Fs],

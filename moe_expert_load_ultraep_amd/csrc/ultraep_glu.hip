@@ -1,7 +1,7 @@
 // gfx950 kernels of the gated activation between the experts' two products and of its
 // gradient rows, quantised on their way out (include/ultraep_layer.h).  Bound by HBM:
 // 32771 rows of 2048, both forms, 403 MB: 72 us, 5.6 TB/s; their gradients, 671 MB:
-// 153 us, 4.4 TB/s (the registers of two halves leave a CU one workgroup; 219 with every
+// 152 us, 4.4 TB/s (the registers of two halves leave a CU one workgroup; 219 with every
 // half read for itself), in rows alone 92 us, 5.9 TB/s.
 #include <hip/hip_runtime.h>
 

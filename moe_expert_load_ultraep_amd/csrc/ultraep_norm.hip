@@ -1,7 +1,7 @@
 // gfx950 kernels of the residual addition with the root-mean-square norm and of its
 // gradients (include/ultraep_layer.h).  Bound by HBM: a row is read once, held in
 // registers and written in all its forms.  32771 rows of 7168, bf16 stream, with the
-// 8-bit form, 2.12 GB: 370 us, 5.7 TB/s (a large copy reaches 5.2); gradients of 16411
+// 8-bit form, 2.12 GB: 365 us, 5.8 TB/s (a large copy reaches 5.2); gradients of 16411
 // rows of 7168, fp32 stream, 1.88 GB: 320 us, 5.9 TB/s.
 #include <hip/hip_runtime.h>
 
@@ -321,7 +321,7 @@ __global__ __launch_bounds__(64 * kSlices) void norm_weight_kernel(const float* 
 constexpr int32_t kTeamOfOne = 512;  // columns up to which a wave has a row of its own
 
 // Workgroups of a pass.  Each reads a row ahead, so that few waves keep the memory busy,
-// and more only stand in each other's way: 256 workgroups of eight waves take 370 us
+// and more only stand in each other's way: 256 workgroups of eight waves take 365 us
 // for 32771 rows of 7168, 512 408; below 4096 columns more are needed (16000 rows of
 // 1024: 2048 workgroups 15.5 us, 512 28.5; of 2048: 512 51, 1024 55).
 int32_t norm_blocks(int32_t H) { return H <= 1024 ? 2048 : H <= 4096 ? 512 : 256; }

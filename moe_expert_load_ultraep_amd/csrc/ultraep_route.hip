@@ -174,7 +174,8 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a, int32
 // v_rcp_f32 are off by a step, so a sigmoid by 3.9, a softmax by 27 with its sum; bias,
 // fma and the cut to whole numbers add 2.5.  Bound by instructions: 262144 tokens of 256
 // experts in 8 groups, 285 MB, 102 us (55 at the rate of a large copy; 95 without any
-// token done again); 524288 of 128 without groups, 302 MB, 75 us.  One wave a token, all in
+// token done again), vector instructions at work in 80 % of the SIMDs' time, LDS in 14 %,
+// its bank conflicts 6 %; 524288 of 128 without groups, 302 MB, 75 us.  One wave a token, all in
 // fp64: 616 and 821.  Logits read a round ahead: 106 and 83, as the chosen ones, read
 // again for their weights, have left the L2 by then.
 template <int LPT, int NI>
@@ -981,8 +982,9 @@ hipError_t launch_route(const RouteArgs& args, int32_t* idx, float* w, hipStream
     // Few tokens: more lanes for each, whose work is done sooner (1024 of 256 experts in
     // groups: 16 lanes 8.5 us, 8 9.3, 4 12.5; 8192: 16.8, 16.3, 19.6).  Many: fewer, which
     // merge less; but with groups of many experts their keys fill LDS, and smaller rounds let
-    // more waves in (262144 tokens of 256 experts: 8 lanes 102 us, 4 105; 65536 of 160 in
-    // groups: 29 and 26; 524288 of 128 without groups: 98 and 75).
+    // more waves in (262144 tokens of 256 experts: 8 lanes 102 us, 4 105; 65536 of 144, 160,
+    // 176, 192, 208, 240 and 256 in groups: 31, 30, 30, 30, 33, 34, 30 and 26, 26, 31, 30, 35,
+    // 37, 30; of 144, 176, 224 and 256 without: 19, 20, 20, 20 and 13, 16, 18, 18).
     const int lanes = a.E > 256 ? 8 : a.tokens <= 4096 ? 16 : a.tokens <= 16384 || (a.groups > 1 && a.E > 160) ? 8 : 4;
     const auto go = lanes == 16  ? (a.E <= 128 ? launch_fast_of<16, 2> : launch_fast_of<16, 4>)
                     : lanes == 8 ? (a.E <= 128   ? launch_fast_of<8, 4>
